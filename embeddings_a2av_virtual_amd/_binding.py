@@ -28,6 +28,12 @@ __all__ = [
     "moe_dispatch_grouped", "moe_combine_grouped_workspace_bytes", "moe_combine_grouped",
     "moe_pack_dispatch_workspace_bytes", "moe_pack_dispatch", "moe_unpack_return_workspace_bytes",
     "moe_unpack_return", "moe_combine_return_workspace_bytes", "moe_combine_return",
+    "moe_route", "moe_route_backward", "moe_combine_backward_workspace_bytes",
+    "moe_combine_backward", "moe_combine_return_backward_workspace_bytes",
+    "moe_combine_return_backward", "moe_expert_linear_workspace_bytes", "moe_expert_linear",
+    "moe_expert_linear_backward_workspace_bytes", "moe_expert_linear_backward",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU",
+    "ACT_SWIGLU", "MAX_WIDTH",
     "keys_bucketize_workspace_bytes",
     "keys_bucketize", "keys_exchange_workspace_bytes", "keys_exchange",
     "keys_exchange_noalloc", "NOALLOC_SCRATCH_BYTES", "a2av_device_copy",
@@ -50,6 +56,10 @@ ST_RECV_OVERFLOW = 4
 ST_BAD_EXPERT = 8
 ST_BAD_OFFSETS = 16
 ST_BAD_PERM = 32
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU, ACT_SWIGLU = range(5)
+MAX_WIDTH = 1 << 20
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _lib = None
 
@@ -107,6 +117,26 @@ def lib():
         L.moe_combine_return_workspace_bytes.restype = sz
         L.moe_combine_return.argtypes = [i32, i64, i32, i32, i64, vp, vpp, vpp, vpp, i64p, vpp, vpp,
                                          i32, vp, sz, vp, vp]
+        L.moe_route.argtypes = [i32, i64, i32, i32, i32, i32, vpp, vp, i32, i32, i32, i32,
+                                ctypes.c_float, vpp, vpp, vp, vp]
+        L.moe_route_backward.argtypes = [i32, i64, i32, i32, i32, i32, vpp, vpp, vpp, i32,
+                                         ctypes.c_float, vpp, vpp, vp, vp]
+        L.moe_combine_backward_workspace_bytes.argtypes = [i32, i64, i32]
+        L.moe_combine_backward_workspace_bytes.restype = sz
+        L.moe_combine_backward.argtypes = [i32, i64, i32, i64, vpp, vpp, vpp, vpp, vpp, vpp, vp, sz,
+                                           vp, vp]
+        L.moe_combine_return_backward_workspace_bytes.argtypes = [i32, i64, i32, i32]
+        L.moe_combine_return_backward_workspace_bytes.restype = sz
+        L.moe_combine_return_backward.argtypes = [i32, i64, i32, i32, i64, vp, vpp, vpp, vpp, i64p,
+                                                  vpp, vpp, vpp, vpp, i32, vp, sz, vp, vp]
+        L.moe_expert_linear_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i64p]
+        L.moe_expert_linear_workspace_bytes.restype = sz
+        L.moe_expert_linear.argtypes = [i32, i32, i64, i64, i32, i32, vpp, i64p, vp, vpp, vpp, vpp,
+                                        vpp, vpp, vp, sz, vp, vp]
+        L.moe_expert_linear_backward_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i64p]
+        L.moe_expert_linear_backward_workspace_bytes.restype = sz
+        L.moe_expert_linear_backward.argtypes = [i32, i32, i64, i64, i32, i32, vpp, i64p, vp, vpp,
+                                                 vpp, vpp, vpp, vpp, vpp, vpp, vp, sz, vp, vp]
         L.keys_bucketize_workspace_bytes.argtypes = [i32, i32]
         L.keys_bucketize_workspace_bytes.restype = sz
         L.keys_bucketize.argtypes = [i32, i32, i64, vpp, vpp, i64p, vpp, vpp, vp, vp, vp, sz, vp,
@@ -123,7 +153,9 @@ def lib():
         for f in ("a2av_exchange_splits", "a2av_offsets", "a2av_copy", "a2av_all_to_all_vdev",
                   "moe_pack", "moe_unpack", "moe_combine", "moe_regroup", "moe_dispatch_grouped",
                   "moe_combine_grouped", "moe_pack_dispatch", "moe_unpack_return",
-                  "moe_combine_return",
+                  "moe_combine_return", "moe_route", "moe_route_backward",
+                  "moe_combine_backward", "moe_combine_return_backward", "moe_expert_linear",
+                  "moe_expert_linear_backward",
                   "keys_bucketize", "keys_exchange", "keys_exchange_noalloc",
                   "a2av_device_copy", "a2av_device_read", "a2av_device_fill"):
             getattr(L, f).restype = i32
@@ -162,9 +194,46 @@ def _i64_array(vals):
     return arr
 
 
+def _typed(tensors, name, dtype, sizes):
+    """Pointers of one array per rank (None: no arrays), each on the GPU,
+    contiguous, of this type and with at least this many elements."""
+    if tensors is None:
+        return None
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name} needs {len(sizes)} entries")
+    arr = (ctypes.c_void_p * len(sizes))()
+    for i, (t, n) in enumerate(zip(tensors, sizes)):
+        if t is None:
+            if n > 0:
+                raise ValueError(f"{name}[{i}] needs {n} elements")
+            continue
+        arr[i] = _one(t, f"{name}[{i}]", dtype, n)
+    return arr
+
+
+def _one(t, name, dtype, n):
+    p = _dev(t, name)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name} needs {n} elements, has {t.numel()}")
+    return p
+
+
 def _check(fn, rc):
     if rc != OK:
         raise A2avError(fn, rc)
+
+
+def _call(fn, like, *args):
+    """The C entry point with the tensors' GPU current: the kernels of a stream
+    are launched on the GPU that is current."""
+    f = getattr(lib(), fn)
+    if like.device.index == torch.cuda.current_device():
+        _check(fn, f(*args))
+        return
+    with torch.cuda.device(like.device):
+        _check(fn, f(*args))
 
 
 # ------------------------------------------------------------------ entry points
@@ -375,6 +444,141 @@ def moe_combine_return(W, T, k, E, H, expert_counts, ids, perm, recv, recv_rows,
                                     _dev(workspace, "workspace"),
                                     workspace.numel() * workspace.element_size(),
                                     _dev(status, "status"), _stream(stream, status)))
+
+
+def moe_route(W, T, k, E, score, logits, bias, groups, topk_groups, group_top, renorm, scale, ids,
+              weights, status, stream=None):
+    """Expert ids (int32 [T, k] per rank) and gate weights (fp32) from router
+    logits [T, E] (fp32, bf16 or fp16): softmax or sigmoid scores, a selection
+    bias (fp32 [E] or None), the best topk_groups of groups, the k best
+    experts, renormalised and scaled."""
+    dtype = _logits_type(logits)
+    _call("moe_route", status, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
+          _typed(logits, "logits", dtype, [T * E] * W),
+          None if bias is None else _one(bias, "bias", torch.float32, E), int(groups),
+          int(topk_groups), int(group_top), int(bool(renorm)), float(scale),
+          _typed(ids, "ids", torch.int32, [T * k] * W),
+          _typed(weights, "weights", torch.float32, [T * k] * W), _dev(status, "status"),
+          _stream(stream, status))
+
+
+def moe_route_backward(W, T, k, E, score, logits, ids, weights, renorm, scale, d_weights, d_logits,
+                       status, stream=None):
+    """The gradient of moe_route's weights in its logits, the ids held fixed."""
+    dtype = _logits_type(logits)
+    _call("moe_route_backward", status, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
+          _typed(logits, "logits", dtype, [T * E] * W),
+          _typed(ids, "ids", torch.int32, [T * k] * W),
+          _typed(weights, "weights", torch.float32, [T * k] * W), int(bool(renorm)), float(scale),
+          _typed(d_weights, "d_weights", torch.float32, [T * k] * W),
+          _typed(d_logits, "d_logits", dtype, [T * E] * W), _dev(status, "status"),
+          _stream(stream, status))
+
+
+def _logits_type(logits):
+    if not logits or not isinstance(logits[0], torch.Tensor) or logits[0].dtype not in _TYPES:
+        raise ValueError("logits must be a list of fp32, bf16 or fp16 tensors, one per rank")
+    return logits[0].dtype
+
+
+def moe_combine_backward_workspace_bytes(W, T, k) -> int:
+    return int(lib().moe_combine_backward_workspace_bytes(int(W), int(T), int(k)))
+
+
+def moe_combine_backward(W, T, k, H, back, perm, weights, d_out, d_back, d_weights, workspace,
+                         status, stream=None):
+    """The gradient of moe_combine in its rows (d_back, bf16) and its weights
+    (d_weights, fp32), from d_out (bf16 [T, H] per rank)."""
+    bf16, rows, toks = torch.bfloat16, [T * k * H] * W, [T * H] * W
+    _call("moe_combine_backward", status, int(W), int(T), int(k), int(H),
+          _typed(back, "back", bf16, rows), _typed(perm, "perm", torch.int64, [T * k] * W),
+          _typed(weights, "weights", torch.float32, [T * k] * W),
+          _typed(d_out, "d_out", bf16, toks), _typed(d_back, "d_back", bf16, rows),
+          _typed(d_weights, "d_weights", torch.float32, [T * k] * W),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"), _stream(stream, status))
+
+
+def moe_combine_return_backward_workspace_bytes(W, T, k, E) -> int:
+    return int(lib().moe_combine_return_backward_workspace_bytes(int(W), int(T), int(k), int(E)))
+
+
+def moe_combine_return_backward(W, T, k, E, H, expert_counts, ids, perm, recv, recv_rows, weights,
+                                d_out, d_recv, d_weights, layout, workspace, status, stream=None):
+    """The gradient of moe_combine_return: every slot's row read, and its
+    gradient written, at the owner of its expert."""
+    bf16, rows = torch.bfloat16, [int(n) * H for n in recv_rows]
+    if len(rows) != W:
+        raise ValueError("recv_rows needs W entries")
+    _call("moe_combine_return_backward", status, int(W), int(T), int(k), int(E), int(H),
+          _one(expert_counts, "expert_counts", torch.int64, W * E),
+          _typed(ids, "ids", torch.int32, [T * k] * W),
+          _typed(perm, "perm", torch.int64, [T * k] * W), _typed(recv, "recv", bf16, rows),
+          _i64_array(recv_rows), _typed(weights, "weights", torch.float32, [T * k] * W),
+          _typed(d_out, "d_out", bf16, [T * H] * W), _typed(d_recv, "d_recv", bf16, rows),
+          _typed(d_weights, "d_weights", torch.float32, [T * k] * W), int(layout),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"), _stream(stream, status))
+
+
+def _expert_type(x):
+    for t in x:
+        if isinstance(t, torch.Tensor):
+            if t.dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError(f"expert rows must be bf16 or fp16, not {t.dtype}")
+            return t.dtype
+    raise ValueError("x must be a list of tensors, one per rank")
+
+
+def moe_expert_linear_workspace_bytes(W, P, K, N, act, x_rows) -> int:
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    return int(lib().moe_expert_linear_workspace_bytes(int(W), int(P), int(K), int(N), int(act),
+                                                       _i64_array(x_rows)))
+
+
+def moe_expert_linear(W, P, K, N, act, x, x_rows, expert_offsets, weight, bias, residual, out, pre,
+                      workspace, status, stream=None):
+    """out = act(x . weight^T + bias) + residual for the rows of every expert
+    (bf16 or fp16); bias, residual and pre may be None."""
+    dtype, NW = _expert_type(weight), 2 * N if act == ACT_SWIGLU else N
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    narrow, wide = [int(n) * N for n in x_rows], [int(n) * NW for n in x_rows]
+    _call("moe_expert_linear", status, int(W), int(P), int(K), int(N), _TYPES[dtype], int(act),
+          _typed(x, "x", dtype, [int(n) * K for n in x_rows]), _i64_array(x_rows),
+          _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
+          _typed(weight, "weight", dtype, [P * NW * K] * W),
+          _typed(bias, "bias", dtype, [P * NW] * W), _typed(residual, "residual", dtype, narrow),
+          _typed(out, "out", dtype, narrow), _typed(pre, "pre", dtype, wide),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"), _stream(stream, status))
+
+
+def moe_expert_linear_backward_workspace_bytes(W, P, K, N, act, x_rows) -> int:
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    return int(lib().moe_expert_linear_backward_workspace_bytes(int(W), int(P), int(K), int(N),
+                                                                int(act), _i64_array(x_rows)))
+
+
+def moe_expert_linear_backward(W, P, K, N, act, x, x_rows, expert_offsets, weight, pre, d_out,
+                               d_pre, d_x, d_weight, d_bias, workspace, status, stream=None):
+    """The gradients of moe_expert_linear; d_x, d_weight and d_bias may be None
+    (not wanted), pre and d_pre are None with ACT_NONE."""
+    dtype, NW = _expert_type(weight), 2 * N if act == ACT_SWIGLU else N
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    wide, xs, ws = [int(n) * NW for n in x_rows], [int(n) * K for n in x_rows], [P * NW * K] * W
+    _call("moe_expert_linear_backward", status, int(W), int(P), int(K), int(N), _TYPES[dtype],
+          int(act), _typed(x, "x", dtype, xs), _i64_array(x_rows),
+          _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
+          _typed(weight, "weight", dtype, ws), _typed(pre, "pre", dtype, wide),
+          _typed(d_out, "d_out", dtype, [int(n) * N for n in x_rows]),
+          _typed(d_pre, "d_pre", dtype, wide), _typed(d_x, "d_x", dtype, xs),
+          _typed(d_weight, "d_weight", dtype, ws), _typed(d_bias, "d_bias", dtype, [P * NW] * W),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"), _stream(stream, status))
 
 
 def keys_bucketize_workspace_bytes(W, n_tables) -> int:

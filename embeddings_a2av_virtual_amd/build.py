@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liba2av.so")
-SOURCES = ["a2av.hip", "moe.hip", "blocks.hip"]
+SOURCES = ["a2av.hip", "moe.hip", "blocks.hip", "route.hip", "experts.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

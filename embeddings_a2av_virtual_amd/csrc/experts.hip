@@ -1,0 +1,580 @@
+// experts.hip — the experts' products on expert-major rows, and their gradient
+// (gfx950).
+//
+// Rank d's rows lie expert by expert (expert_offsets[d]), so every product is
+// a batch of matrix products whose row counts only the device knows:
+//   forward    out = act(x . W_e^T + b_e) + residual   contraction over K
+//   d_x        d_pre . W_e                             contraction over NW
+//   d_weight   d_pre^T . x                             contraction over rows
+//
+//   k_expert_plan   checks the offsets, lists the row tiles of all experts
+//   k_expert_any    one 64 x 64 tile of one product, any size and alignment
+//   k_expert_dpre   d_pre = d_out * act'(pre), with the bias sums of row blocks
+//   k_expert_dbias  the bias sums of an expert's row blocks, in order
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "common.hpp"
+
+namespace a2av {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+enum { kForward, kDx, kDweight };
+
+// ------------------------------------------------------------------ element types
+struct Bf16 {
+    typedef bf16x8 frag;
+    static __device__ __forceinline__ float to_float(uint16_t v) { return bf16_lo(v); }
+    static __device__ __forceinline__ uint16_t from_float(float f) { return (uint16_t)to_bf16(f); }
+    static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+struct Fp16 {
+    typedef f16x8 frag;
+    static __device__ __forceinline__ float to_float(uint16_t v) {
+        return (float)__builtin_bit_cast(_Float16, v);
+    }
+    static __device__ __forceinline__ uint16_t from_float(float f) {
+        return __builtin_bit_cast(uint16_t, (_Float16)f);
+    }
+    static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// ------------------------------------------------------------------ activations
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + __expf(-x)); }
+
+// act(h) for one product; NaN stays NaN.
+__device__ __forceinline__ float act_of(int act, float h) {
+    switch (act) {
+    case A2AV_ACT_RELU: return h < 0.0f ? 0.0f : h;
+    case A2AV_ACT_GELU: return h * 0.5f * erfcf(h * -0.70710678f);
+    case A2AV_ACT_SILU: return h * sigmoid(h);
+    default: return h;
+    }
+}
+
+// act'(h).
+__device__ __forceinline__ float act_slope(int act, float h) {
+    switch (act) {
+    case A2AV_ACT_RELU: return h <= 0.0f ? 0.0f : 1.0f;
+    case A2AV_ACT_GELU:
+        return 0.5f * erfcf(h * -0.70710678f) + h * 0.39894228f * __expf(-0.5f * h * h);
+    case A2AV_ACT_SILU: {
+        const float s = sigmoid(h);
+        return s * (1.0f + h * (1.0f - s));
+    }
+    default: return 1.0f;
+    }
+}
+
+// ------------------------------------------------------------------ plan
+struct PlanArgs {
+    int64_t x_rows[A2AV_MAX_W];
+    const int64_t *offsets;  // [W][P + 1]
+    int32_t *tiles;          // [0] tile count, then (expert, tile of the expert) pairs
+    int32_t *first;          // [W * P + 1] first tile of each expert
+    int32_t *status;
+    int W, P;
+    int tile_rows;
+};
+
+// One workgroup. Thread t owns up to kPlanPer consecutive experts of the
+// W * P; a scan of their tile counts gives every expert its first tile, and
+// the threads then fill the list tile by tile (a search in the scan), so that
+// one expert with most of the rows does not leave the list to one thread.
+__global__ __launch_bounds__(kPlanThreads) void k_expert_plan(const PlanArgs a) {
+    __shared__ int32_t first[A2AV_MAX_EXPERTS + 1];
+    __shared__ int32_t part[kPlanThreads / kWave];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int n = a.W * a.P;
+    int bad = 0;
+    uint32_t mine[kPlanPer], sum = 0;
+#pragma unroll
+    for (int u = 0; u < kPlanPer; u++) {
+        const int i = tid * kPlanPer + u;
+        mine[u] = 0;
+        if (i < n) {
+            const int d = i / a.P, j = i - d * a.P;
+            const int64_t *off = a.offsets + (int64_t)d * (a.P + 1) + j;
+            const int64_t r0 = off[0], r1 = off[1];
+            if ((j == 0 && r0 != 0) || r0 < 0 || r1 < r0) bad |= A2AV_ST_BAD_OFFSETS;
+            else if (r1 > a.x_rows[d]) bad |= A2AV_ST_SEND_OVERRUN;
+            else mine[u] = (uint32_t)((r1 - r0 + a.tile_rows - 1) / a.tile_rows);
+        }
+        sum += mine[u];
+    }
+    const int off_bad = __syncthreads_or(bad & A2AV_ST_BAD_OFFSETS);
+    const int run_bad = __syncthreads_or(bad & A2AV_ST_SEND_OVERRUN);
+    const int poisoned = __syncthreads_or(tid == 0 ? status_poisoned(a.status) : 0);
+    if (poisoned) return;
+    if (off_bad | run_bad) {
+        // descending offsets alone: what lies past x_rows then says nothing
+        if (tid == 0) atomicOr(a.status, off_bad ? A2AV_ST_BAD_OFFSETS : A2AV_ST_SEND_OVERRUN);
+        return;
+    }
+    const uint32_t inc = wave_incl_scan_u32(sum);
+    if (lane == kWave - 1) part[wave] = (int32_t)inc;
+    __syncthreads();
+    uint32_t at = inc - sum, total = 0;
+    for (int w = 0; w < kPlanThreads / kWave; w++) {
+        if (w < wave) at += (uint32_t)part[w];
+        total += (uint32_t)part[w];
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanPer; u++) {
+        const int i = tid * kPlanPer + u;
+        if (i < n) first[i] = a.first[i] = (int32_t)at;
+        at += mine[u];
+    }
+    if (tid == 0) {
+        first[n] = a.first[n] = (int32_t)total;
+        a.tiles[0] = (int32_t)total;
+    }
+    __syncthreads();
+    for (uint32_t t = tid; t < total; t += kPlanThreads) {
+        int lo = 0, hi = n;  // the last expert whose first tile is at or before t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((uint32_t)first[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        a.tiles[2 + 2 * t] = lo;
+        a.tiles[3 + 2 * t] = (int32_t)t - first[lo];
+    }
+}
+
+// ------------------------------------------------------------------ products
+struct ExpertArgs {
+    const void *a[A2AV_MAX_W];         // x (forward), d_pre (gradients)
+    const void *b[A2AV_MAX_W];         // weight (forward, d_x), x (d_weight)
+    const void *bias[A2AV_MAX_W];      // forward
+    const void *residual[A2AV_MAX_W];  // forward
+    void *out[A2AV_MAX_W];             // out, d_x, d_weight
+    void *pre[A2AV_MAX_W];             // forward
+    const int64_t *offsets;
+    const int32_t *tiles;
+    const int32_t *status;
+    int64_t K, N, NW;
+    int W, P;
+    int act;
+    int has_bias, has_residual, has_pre;
+    int tile_rows;
+};
+
+// The weight row behind column c of the product: with SwiGLU, blocks of 16
+// gate columns and the 16 up columns of the same outputs alternate, so that
+// one lane ends with both.
+__device__ __forceinline__ int64_t weight_row(int64_t c, int64_t N, bool glu) {
+    if (!glu) return c;
+    return ((c >> 4) & 1) * N + ((c >> 5) << 4) + (c & 15);
+}
+
+constexpr int kAny = 64;       // tile rows and columns
+constexpr int kAnyK = 32;      // contraction step
+constexpr int kAnyPad = 40;    // LDS row, in elements
+
+// One 64 x 64 tile by four waves of 32 x 32, elements loaded one by one with
+// their bounds checked; what lies outside is 0 in both operands, so it adds
+// nothing even where the other holds infinities or NaN.
+template <int KIND, typename T>
+__global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
+    __shared__ __align__(16) uint16_t sa[kAny * kAnyPad], sb[kAny * kAnyPad];
+    if (status_at_entry(a.status)) return;
+    int e, mt;
+    if constexpr (KIND == kDweight) {
+        e = blockIdx.z;
+        mt = blockIdx.y;
+    } else {
+        const int t = blockIdx.y + gridDim.y * blockIdx.z;
+        if (t >= a.tiles[0]) return;
+        e = a.tiles[2 + 2 * t];
+        mt = a.tiles[3 + 2 * t];
+    }
+    const int d = e / a.P, j = e - d * a.P;
+    const int64_t row0 = a.offsets[(int64_t)d * (a.P + 1) + j];
+    const int64_t rows = a.offsets[(int64_t)d * (a.P + 1) + j + 1] - row0;
+    const bool glu = KIND == kForward && a.act == A2AV_ACT_SWIGLU;
+    const int64_t M = KIND == kDweight ? a.NW : rows;
+    const int64_t C = KIND == kForward ? (glu ? (a.N + 15) / 16 * 32 : a.N) : a.K;
+    const int64_t L = KIND == kForward ? a.K : KIND == kDx ? a.NW : rows;
+    const int64_t m0 = (int64_t)mt * kAny, c0 = (int64_t)blockIdx.x * kAny;
+    const uint16_t *pa = (const uint16_t *)a.a[d], *pb = (const uint16_t *)a.b[d];
+    if constexpr (KIND == kForward) pa += row0 * a.K;
+    else pa += row0 * a.NW;
+    if constexpr (KIND == kDweight) pb += row0 * a.K;
+    else pb += (int64_t)j * a.NW * a.K;
+    const auto at_a = [&](int64_t m, int64_t k) -> uint16_t {
+        if (m >= M || k >= L) return 0;
+        if constexpr (KIND == kDweight) return pa[k * a.NW + m];
+        return pa[m * L + k];
+    };
+    const auto at_b = [&](int64_t c, int64_t k) -> uint16_t {
+        if (c >= C || k >= L) return 0;
+        if constexpr (KIND == kForward) {
+            const int64_t w = weight_row(c, a.N, glu);
+            if (glu && w - ((c >> 4) & 1) * a.N >= a.N) return 0;
+            return pb[w * a.K + k];
+        }
+        return pb[k * a.K + c];
+    };
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int wm = (wave >> 1) * 32, wc = (wave & 1) * 32;
+    f32x4 acc[2][2] = {};
+    for (int64_t k0 = 0; k0 < L; k0 += kAnyK) {
+#pragma unroll
+        for (int u = 0; u < kAny * kAnyK / 256; u++) {
+            const int i = tid + u * 256;
+            // neighbouring threads along what is contiguous in memory
+            const int ar = KIND == kDweight ? i % kAny : i / kAnyK, ak = KIND == kDweight ? i / kAny : i % kAnyK;
+            const int br = KIND == kForward ? i / kAnyK : i % kAny, bk = KIND == kForward ? i % kAnyK : i / kAny;
+            sa[ar * kAnyPad + ak] = at_a(m0 + ar, k0 + ak);
+            sb[br * kAnyPad + bk] = at_b(c0 + br, k0 + bk);
+        }
+        __syncthreads();
+        typename T::frag fa[2], fb[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            fa[u] = *(const typename T::frag *)&sa[(wm + u * 16 + (lane & 15)) * kAnyPad + (lane >> 4) * 8];
+            fb[u] = *(const typename T::frag *)&sb[(wc + u * 16 + (lane & 15)) * kAnyPad + (lane >> 4) * 8];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int v = 0; v < 2; v++) acc[u][v] = T::mfma(fa[u], fb[v], acc[u][v]);
+        __syncthreads();
+    }
+    // lane l holds column l % 16 and rows (l / 16) * 4 .. + 3 of each 16 x 16
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int64_t m = m0 + wm + u * 16 + (lane >> 4) * 4 + i;
+            if (m >= M) continue;
+            if constexpr (KIND == kForward) {
+                const int64_t row = row0 + m;
+                const uint16_t *bias = (const uint16_t *)a.bias[d] + (int64_t)j * a.NW;
+                float y[2];
+                int64_t n[2];
+                int outs = 2;
+                if (glu) {
+                    n[0] = ((c0 + wc) >> 1) + (lane & 15);
+                    if (n[0] >= a.N) continue;
+                    float h0 = acc[u][0][i], h1 = acc[u][1][i];
+                    if (a.has_bias) {
+                        h0 += T::to_float(bias[n[0]]);
+                        h1 += T::to_float(bias[a.N + n[0]]);
+                    }
+                    if (a.has_pre) {
+                        uint16_t *pre = (uint16_t *)a.pre[d] + row * a.NW;
+                        pre[n[0]] = T::from_float(h0);
+                        pre[a.N + n[0]] = T::from_float(h1);
+                    }
+                    y[0] = h0 * sigmoid(h0) * h1;
+                    outs = 1;
+                } else {
+                    for (int v = 0; v < 2; v++) {
+                        n[v] = c0 + wc + v * 16 + (lane & 15);
+                        float h = acc[u][v][i];
+                        if (n[v] < a.N) {
+                            if (a.has_bias) h += T::to_float(bias[n[v]]);
+                            if (a.has_pre) ((uint16_t *)a.pre[d])[row * a.NW + n[v]] = T::from_float(h);
+                        }
+                        y[v] = act_of(a.act, h);
+                    }
+                }
+                for (int v = 0; v < outs; v++) {
+                    if (n[v] >= a.N) continue;
+                    if (a.has_residual) y[v] += T::to_float(((const uint16_t *)a.residual[d])[row * a.N + n[v]]);
+                    ((uint16_t *)a.out[d])[row * a.N + n[v]] = T::from_float(y[v]);
+                }
+            } else {
+                uint16_t *out = (uint16_t *)a.out[d] + (KIND == kDx ? (row0 + m) * a.K : ((int64_t)j * a.NW + m) * a.K);
+#pragma unroll
+                for (int v = 0; v < 2; v++) {
+                    const int64_t c = c0 + wc + v * 16 + (lane & 15);
+                    if (c < C) out[c] = T::from_float(acc[u][v][i]);
+                }
+            }
+        }
+}
+
+// ------------------------------------------------------------------ d_pre and the bias
+struct DpreArgs {
+    const void *pre[A2AV_MAX_W];
+    const void *d_out[A2AV_MAX_W];
+    void *d_pre[A2AV_MAX_W];
+    void *d_bias[A2AV_MAX_W];
+    const int64_t *offsets;
+    const int32_t *tiles;
+    const int32_t *first;
+    float *part;  // [tile][NW] bias sums of the row blocks
+    const int32_t *status;
+    int64_t N, NW;
+    int W, P;
+    int act;
+    int has_bias;
+    int tile_rows;
+};
+
+// One workgroup per (row block, 256 output columns): a thread walks its
+// column down the block's rows.
+template <typename T>
+__global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
+    if (status_at_entry(a.status)) return;
+    const int t = blockIdx.y + gridDim.y * blockIdx.z;
+    if (t >= a.tiles[0]) return;
+    const int e = a.tiles[2 + 2 * t], mt = a.tiles[3 + 2 * t];
+    const int d = e / a.P, j = e - d * a.P;
+    const int64_t *off = a.offsets + (int64_t)d * (a.P + 1) + j;
+    const int64_t r0 = off[0] + (int64_t)mt * a.tile_rows;
+    const int64_t r1 = r0 + a.tile_rows < off[1] ? r0 + a.tile_rows : off[1];
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= a.N) return;
+    const bool glu = a.act == A2AV_ACT_SWIGLU;
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int64_t r = r0; r < r1; r++) {
+        const float g = T::to_float(((const uint16_t *)a.d_out[d])[r * a.N + n]);
+        if (a.act == A2AV_ACT_NONE) {
+            s0 += g;
+            continue;
+        }
+        const uint16_t *pre = (const uint16_t *)a.pre[d] + r * a.NW;
+        uint16_t *d_pre = (uint16_t *)a.d_pre[d] + r * a.NW;
+        const float h = T::to_float(pre[n]);
+        if (glu) {
+            const float up = T::to_float(pre[a.N + n]);
+            const float dg = g * up * act_slope(A2AV_ACT_SILU, h), du = g * h * sigmoid(h);
+            d_pre[n] = T::from_float(dg);
+            d_pre[a.N + n] = T::from_float(du);
+            s0 += dg;
+            s1 += du;
+        } else {
+            const float dh = g * act_slope(a.act, h);
+            d_pre[n] = T::from_float(dh);
+            s0 += dh;
+        }
+    }
+    if (a.has_bias) {
+        a.part[(int64_t)t * a.NW + n] = s0;
+        if (glu) a.part[(int64_t)t * a.NW + a.N + n] = s1;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_expert_dbias(const DpreArgs a) {
+    if (status_at_entry(a.status)) return;
+    const int e = blockIdx.y, d = e / a.P, j = e - d * a.P;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= a.NW) return;
+    float s = 0.0f;
+    for (int t = a.first[e]; t < a.first[e + 1]; t++) s += a.part[(int64_t)t * a.NW + n];
+    ((uint16_t *)a.d_bias[d])[(int64_t)j * a.NW + n] = T::from_float(s);
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kBlockRows = 64;   // row blocks of the bias sums
+
+static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// Row tiles of tile_rows that W * P experts with these rows can have, at most;
+// -1 for sizes that are not valid.
+static int64_t tile_bound(int W, int P, int64_t K, int64_t N, int act, const int64_t *x_rows, int tile_rows) {
+    if (W < 1 || W > A2AV_MAX_W || P < 1 || (int64_t)W * P > A2AV_MAX_EXPERTS || K < 1 || N < 1 || !x_rows)
+        return -1;
+    if (act < A2AV_ACT_NONE || act > A2AV_ACT_SWIGLU) return -1;
+    if (K > A2AV_MAX_WIDTH || N > A2AV_MAX_WIDTH) return -1;
+    int64_t total = 0;
+    for (int d = 0; d < W; d++) {
+        if (x_rows[d] < 0 || x_rows[d] > ((int64_t)1 << 40)) return -1;
+        total += x_rows[d];
+    }
+    const int64_t t = total / tile_rows + (int64_t)W * P;
+    return t <= (1 << 30) ? t : -1;
+}
+
+struct Layout {
+    int64_t tiles;      // tile bound
+    size_t first, part; // byte offsets
+    size_t total;
+};
+
+static bool plan_layout(int W, int P, int64_t K, int64_t N, int act, const int64_t *x_rows,
+                        int tile_rows, bool with_part, Layout *l) {
+    l->tiles = tile_bound(W, P, K, N, act, x_rows, tile_rows);
+    if (l->tiles < 0) return false;
+    l->first = round256((size_t)(l->tiles + 1) * 8);
+    l->part = l->first + round256(((size_t)W * P + 1) * 4);
+    const int64_t NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
+    l->total = l->part + (with_part ? round256((size_t)l->tiles * (size_t)NW * 4) : 0) + 256;
+    return true;
+}
+
+static void launch_plan(int W, int P, const int64_t *x_rows, const int64_t *offsets, int tile_rows,
+                        unsigned char *ws, const Layout &l, int32_t *status, hipStream_t stream) {
+    PlanArgs p;
+    std::memset(&p, 0, sizeof(p));
+    for (int d = 0; d < W; d++) p.x_rows[d] = x_rows[d];
+    p.offsets = offsets;
+    p.tiles = (int32_t *)ws;
+    p.first = (int32_t *)(ws + l.first);
+    p.status = status;
+    p.W = W;
+    p.P = P;
+    p.tile_rows = tile_rows;
+    hipLaunchKernelGGL(k_expert_plan, dim3(1), dim3(kPlanThreads), 0, stream, p);
+}
+
+// Tiles over the y and z dimensions of a grid.
+static dim3 tile_grid(int64_t columns, int64_t tiles) {
+    const int64_t y = tiles < 32768 ? tiles : 32768;
+    return dim3((unsigned)columns, (unsigned)y, (unsigned)((tiles + y - 1) / y));
+}
+
+template <int KIND>
+static void launch_product(const ExpertArgs &a, int type, int64_t tiles, hipStream_t stream) {
+    dim3 g;
+    if (KIND == kDweight)
+        g = dim3((unsigned)((a.K + kAny - 1) / kAny), (unsigned)((a.NW + kAny - 1) / kAny), a.W * a.P);
+    else {
+        int64_t cols = KIND == kDx ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
+        g = tile_grid((cols + kAny - 1) / kAny, tiles);
+    }
+    if (type == A2AV_DT_BF16) hipLaunchKernelGGL((k_expert_any<KIND, Bf16>), g, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_expert_any<KIND, Fp16>), g, dim3(256), 0, stream, a);
+}
+
+static bool fits(int64_t rows, int64_t width) {
+    return (uint64_t)rows <= (uint64_t)INT64_MAX / 4 / (uint64_t)width;
+}
+
+}  // namespace a2av
+
+using namespace a2av;
+
+A2AV_API size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int act,
+                                                  const int64_t *x_rows) {
+    Layout l;
+    return plan_layout(W, P, K, N, act, x_rows, kAny, false, &l) ? l.total : 0;
+}
+
+A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int act,
+                               const void *const *x, const int64_t *x_rows,
+                               const int64_t *expert_offsets, const void *const *weight,
+                               const void *const *bias, const void *const *residual,
+                               void *const *out, void *const *pre, void *workspace,
+                               size_t workspace_bytes, int32_t *status, hipStream_t stream) {
+    Layout l;
+    if (!plan_layout(W, P, K, N, act, x_rows, kAny, false, &l)) return A2AV_EARG;
+    if ((type != A2AV_DT_BF16 && type != A2AV_DT_F16) || !x || !expert_offsets || !weight || !out || !status)
+        return A2AV_EARG;
+    if (!workspace || (uintptr_t)workspace % 8 != 0 || workspace_bytes < l.total) return A2AV_EARG;
+    ExpertArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.K = K;
+    a.N = N;
+    a.NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
+    for (int d = 0; d < W; d++) {
+        if (!fits(x_rows[d], K) || !fits(x_rows[d], a.NW)) return A2AV_EARG;
+        if (!weight[d] || (bias && !bias[d])) return A2AV_EARG;
+        if (x_rows[d] > 0 && (!x[d] || !out[d] || (residual && !residual[d]) || (pre && !pre[d])))
+            return A2AV_EARG;
+        a.a[d] = x[d];
+        a.b[d] = weight[d];
+        a.bias[d] = bias ? bias[d] : nullptr;
+        a.residual[d] = residual ? residual[d] : nullptr;
+        a.out[d] = out[d];
+        a.pre[d] = pre ? pre[d] : nullptr;
+    }
+    a.offsets = expert_offsets;
+    a.tiles = (const int32_t *)workspace;
+    a.status = status;
+    a.W = W;
+    a.P = P;
+    a.act = act;
+    a.has_bias = bias != nullptr;
+    a.has_residual = residual != nullptr;
+    a.has_pre = pre != nullptr;
+    launch_plan(W, P, x_rows, expert_offsets, kAny, (unsigned char *)workspace, l, status, stream);
+    launch_product<kForward>(a, type, l.tiles, stream);
+    return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
+}
+
+A2AV_API size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64_t N,
+                                                           int act, const int64_t *x_rows) {
+    Layout l;
+    return plan_layout(W, P, K, N, act, x_rows, kBlockRows, true, &l) ? l.total : 0;
+}
+
+A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int type, int act,
+                                        const void *const *x, const int64_t *x_rows,
+                                        const int64_t *expert_offsets, const void *const *weight,
+                                        const void *const *pre, const void *const *d_out,
+                                        void *const *d_pre, void *const *d_x, void *const *d_weight,
+                                        void *const *d_bias, void *workspace,
+                                        size_t workspace_bytes, int32_t *status,
+                                        hipStream_t stream) {
+    Layout l;
+    if (!plan_layout(W, P, K, N, act, x_rows, kBlockRows, true, &l)) return A2AV_EARG;
+    const bool none = act == A2AV_ACT_NONE;
+    if ((type != A2AV_DT_BF16 && type != A2AV_DT_F16) || !x || !expert_offsets || !weight || !d_out || !status)
+        return A2AV_EARG;
+    if (none ? (pre || d_pre) : (!pre || !d_pre)) return A2AV_EARG;
+    if (!workspace || (uintptr_t)workspace % 8 != 0 || workspace_bytes < l.total) return A2AV_EARG;
+    unsigned char *ws = (unsigned char *)workspace;
+    ExpertArgs a, b;
+    DpreArgs g;
+    std::memset(&a, 0, sizeof(a));
+    std::memset(&b, 0, sizeof(b));
+    std::memset(&g, 0, sizeof(g));
+    a.K = K;
+    a.N = g.N = N;
+    a.NW = g.NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
+    a.offsets = g.offsets = expert_offsets;
+    a.tiles = g.tiles = (const int32_t *)ws;
+    a.status = g.status = status;
+    a.W = g.W = W;
+    a.P = g.P = P;
+    a.act = g.act = act;
+    b = a;
+    g.first = (const int32_t *)(ws + l.first);
+    g.part = (float *)(ws + l.part);
+    g.has_bias = d_bias != nullptr;
+    g.tile_rows = kBlockRows;
+    for (int d = 0; d < W; d++) {
+        if (!fits(x_rows[d], K) || !fits(x_rows[d], a.NW)) return A2AV_EARG;
+        if (!weight[d] || (d_weight && !d_weight[d]) || (d_bias && !d_bias[d])) return A2AV_EARG;
+        if (x_rows[d] > 0 && (!x[d] || !d_out[d] || (!none && (!pre[d] || !d_pre[d])) || (d_x && !d_x[d])))
+            return A2AV_EARG;
+        g.pre[d] = none ? nullptr : pre[d];
+        g.d_out[d] = d_out[d];
+        g.d_pre[d] = none ? nullptr : d_pre[d];
+        g.d_bias[d] = d_bias ? d_bias[d] : nullptr;
+        a.a[d] = b.a[d] = none ? d_out[d] : d_pre[d];
+        a.b[d] = weight[d];
+        a.out[d] = d_x ? d_x[d] : nullptr;
+        b.b[d] = x[d];
+        b.out[d] = d_weight ? d_weight[d] : nullptr;
+    }
+    launch_plan(W, P, x_rows, expert_offsets, kBlockRows, ws, l, status, stream);
+    if (!none || d_bias) {
+        const dim3 grid = tile_grid((N + 255) / 256, l.tiles);
+        if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dpre<Bf16>, grid, dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL(k_expert_dpre<Fp16>, grid, dim3(256), 0, stream, g);
+    }
+    if (d_bias) {
+        const dim3 grid((unsigned)((a.NW + 255) / 256), W * P);
+        if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dbias<Bf16>, grid, dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL(k_expert_dbias<Fp16>, grid, dim3(256), 0, stream, g);
+    }
+    if (d_x) launch_product<kDx>(a, type, l.tiles, stream);
+    if (d_weight) launch_product<kDweight>(b, type, l.tiles, stream);
+    return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
+}

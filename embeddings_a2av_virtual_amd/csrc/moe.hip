@@ -14,6 +14,7 @@
 //   k_moe_scatter token-major row scatter: read each token once, write it to
 //                 its k packed rows
 //   k_perm_check + k_moe_gather   the un-pack: out[q] = back[perm[q]]
+//   k_perm_mark, k_mark_check, k_combine_backward   the combine's gradient
 #include <hip/hip_runtime.h>
 
 #include <cstring>
@@ -489,6 +490,7 @@ struct ReturnArgs {
     const uint64_t *row_addr;  // [W][E] (plan)
     const int64_t *ystart;     // [W][E] (plan)
     uint64_t *xaddr;           // [W][T*k] each slot's row address, or null
+    int32_t *mark;             // [W][T*k] the slot that has each pack row, or null
     int32_t *words;            // [0] plan bits, [1] slot bits
     int32_t *status;
     uint64_t R;
@@ -519,8 +521,13 @@ __global__ __launch_bounds__(256) void k_slot_check(const ReturnArgs a) {
             const int64_t cn = a.counts[(int64_t)s * a.E + e];
             const uint64_t ra = a.xaddr ? a.row_addr[(int64_t)s * a.E + e] : 0;
             const int64_t p = pq - ys;
-            if (p < 0 || p >= cn) bad = A2AV_ST_BAD_PERM;
-            else if (a.xaddr) a.xaddr[(int64_t)s * a.Q + q] = ra + (uint64_t)pq * a.R;
+            // counts that do not come from these ids may allow rows past Q,
+            // which have no mark
+            if (p < 0 || p >= cn || (a.mark && (uint64_t)pq >= (uint64_t)a.Q)) bad = A2AV_ST_BAD_PERM;
+            else {
+                if (a.xaddr) a.xaddr[(int64_t)s * a.Q + q] = ra + (uint64_t)pq * a.R;
+                if (a.mark) a.mark[(int64_t)s * a.Q + pq] = (int32_t)q;
+            }
         }
     }
     const int be = __ballot(bad & A2AV_ST_BAD_EXPERT) != 0, bp = __ballot(bad & A2AV_ST_BAD_PERM) != 0;
@@ -755,6 +762,152 @@ __global__ __launch_bounds__(256) void k_moe_combine_any(const CombineArgs a) {
             dst[h] = (uint16_t)to_bf16(acc);
         }
     }
+}
+
+// ------------------------------------------------------------------ combine's gradient
+// d_row = bf16(w * d_out[t]) for every slot's row, and d_w = <row, d_out[t]>
+// with fp32 products and sums. The rows are written where the combine read
+// them, so two slots that name one row would race: each slot writes its number
+// to its row's mark, and a slot that then finds another number there shares
+// its row (one of the two always does, whatever order the writes took).
+struct CombineGradArgs {
+    const unsigned char *rows[A2AV_MAX_W];   // per source (pack order) or per owner
+    const int64_t *perm[A2AV_MAX_W];
+    const float *w[A2AV_MAX_W];
+    const unsigned char *d_out[A2AV_MAX_W];
+    unsigned char *d_rows[A2AV_MAX_W];
+    float *d_w[A2AV_MAX_W];
+    const int32_t *ids[A2AV_MAX_W];          // HOME only
+    int32_t *mark;                           // [W][T*k]
+    const uint64_t *xaddr;                   // HOME: [W][T*k] row addresses
+    int32_t *words;                          // HOME: [0] plan bits, [1] slot bits
+    int32_t *status;
+    int64_t T;
+    int64_t H;
+    int k;
+    int W;
+    int P;                                   // HOME: experts per owner
+};
+
+__global__ __launch_bounds__(256) void k_perm_mark(const CombineGradArgs a) {
+    if (status_poisoned(a.status)) return;
+    const int r = blockIdx.y;
+    const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, Q = a.T * a.k;
+    int bad = 0;
+    if (q < Q) {
+        const int64_t p = a.perm[r][q];
+        bad = p < 0 || p >= Q;
+        if (!bad) a.mark[(int64_t)r * Q + p] = (int32_t)q;
+    }
+    if (__ballot(bad) != 0 && (threadIdx.x & (kWave - 1)) == 0) atomicOr(a.status, A2AV_ST_BAD_PERM);
+}
+
+template <bool HOME>
+__global__ __launch_bounds__(256) void k_mark_check(const CombineGradArgs a) {
+    if (status_poisoned(a.status)) return;  // also a perm entry out of range
+    if constexpr (HOME) {
+        // slots without a mark: nothing to compare, the verdict stands
+        if (a.words[0] | __hip_atomic_load(&a.words[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) return;
+    }
+    const int r = blockIdx.y;
+    const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, Q = a.T * a.k;
+    int bad = 0;
+    if (q < Q) bad = a.mark[(int64_t)r * Q + a.perm[r][q]] != (int32_t)q;
+    if (__ballot(bad) != 0 && (threadIdx.x & (kWave - 1)) == 0)
+        atomicOr(HOME ? &a.words[1] : a.status, A2AV_ST_BAD_PERM);
+}
+
+// One workgroup per token; its waves take the token's slots in turn, so the
+// token's d_out comes from HBM once and from the L1 for the other slots.
+// Moves 2 * k + 1 rows per token and is bound by that traffic.
+template <bool HOME, bool ALIGNED>
+__global__ __launch_bounds__(512) void k_combine_backward(const CombineGradArgs a) {
+    if (status_at_entry(a.status)) return;
+    if constexpr (HOME) {
+        const int32_t pb = *(const const_i32 *)&a.words[0];
+        const int32_t cw = *(const const_i32 *)&a.words[1];
+        if (pb | cw) {
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                atomicOr(a.status, (pb & A2AV_ST_BAD_SPLIT) ? A2AV_ST_BAD_SPLIT : (pb | cw));
+            return;
+        }
+    }
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
+    const uint64_t n = (uint64_t)a.W * (uint64_t)a.T, rowb = (uint64_t)a.H * 2;
+    const int k = a.k;
+    for (uint64_t tok = blockIdx.x; tok < n; tok += gridDim.x) {
+        const int r = (int)(tok / (uint64_t)a.T);
+        const int64_t t = (int64_t)(tok - (uint64_t)r * (uint64_t)a.T);
+        const unsigned char *g = a.d_out[r] + (uint64_t)t * rowb;
+        for (int j = wave; j < k; j += waves) {
+            const int64_t q = t * k + j;
+            const float w = a.w[r][q];
+            const unsigned char *src;
+            unsigned char *dst;
+            if constexpr (HOME) {
+                const uint64_t x = a.xaddr[(uint64_t)r * a.T * k + q];
+                const int d = a.ids[r][q] / a.P;
+                src = (const unsigned char *)(uintptr_t)x;
+                dst = a.d_rows[d] + (x - (uint64_t)(uintptr_t)a.rows[d]);
+            } else {
+                const uint64_t off = (uint64_t)a.perm[r][q] * rowb;
+                src = a.rows[r] + off;
+                dst = a.d_rows[r] + off;
+            }
+            float acc = 0.0f;
+            if constexpr (ALIGNED) {
+                const uint64_t nv = rowb / 16;
+                constexpr int U = 4;
+                for (uint64_t i0 = 0; i0 < nv; i0 += U * kWave) {
+                    u32x4 x[U], y[U];
+#pragma unroll
+                    for (int u = 0; u < U; u++) {
+                        uint64_t i = i0 + u * kWave + lane;
+                        i = i < nv ? i : nv - 1;
+                        x[u] = ld<true>((const u32x4 *)src + i);
+                        y[u] = ((const u32x4 *)g)[i];
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; u++) {
+                        const uint64_t i = i0 + u * kWave + lane;
+                        if (i < nv) {
+                            u32x4 o;
+#pragma unroll
+                            for (int c = 0; c < 4; c++) {
+                                const float lo = bf16_lo(y[u][c]), hi = bf16_hi(y[u][c]);
+                                acc = __builtin_fmaf(bf16_lo(x[u][c]), lo, acc);
+                                acc = __builtin_fmaf(bf16_hi(x[u][c]), hi, acc);
+                                o[c] = to_bf16(w * lo) | (to_bf16(w * hi) << 16);
+                            }
+                            st<true>((u32x4 *)dst + i, o);
+                        }
+                    }
+                }
+            } else {
+                for (uint64_t h = lane; h < (uint64_t)a.H; h += kWave) {
+                    const float y = bf16_lo(((const uint16_t *)g)[h]);
+                    acc = __builtin_fmaf(bf16_lo(((const uint16_t *)src)[h]), y, acc);
+                    ((uint16_t *)dst)[h] = (uint16_t)to_bf16(w * y);
+                }
+            }
+#pragma unroll
+            for (int o = 32; o; o >>= 1) acc += __shfl_xor(acc, o);
+            if (lane == 0) a.d_w[r][q] = acc;
+        }
+    }
+}
+
+template <bool HOME>
+static void launch_combine_backward(const CombineGradArgs &a, bool aligned, hipStream_t stream) {
+    // as many waves as a token has slots, up to eight
+    const int waves = a.k >= 8 ? 8 : a.k >= 4 ? 4 : a.k;
+    uint64_t blocks = (uint64_t)a.W * (uint64_t)a.T;
+    if (blocks < 1) blocks = 1;  // a verdict of the plan is reported
+    if (blocks > max_grid()) blocks = max_grid();
+    const dim3 g((unsigned)blocks), b(waves * kWave);
+    if (aligned) hipLaunchKernelGGL((k_combine_backward<HOME, true>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_combine_backward<HOME, false>), g, b, 0, stream, a);
 }
 
 static int64_t n_segments(int64_t Q) { return (Q + kSeg - 1) / kSeg; }
@@ -1204,5 +1357,150 @@ A2AV_API int moe_combine(int W, int64_t T, int k, int64_t H, const void *const *
                                (unsigned)env_long("A2AV_COMBINE_LDS", kCombineLds, 0, 65536), stream, a,
                                nchunk);
     }
+    return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
+}
+
+A2AV_API size_t moe_combine_backward_workspace_bytes(int W, int64_t T, int k) {
+    if (W < 1 || W > A2AV_MAX_W || T < 0 || k < 1) return 0;
+    if (T > ((int64_t)1 << 31) / k || T * k >= ((int64_t)1 << 31)) return 0;
+    return round256((size_t)W * (size_t)(T * k) * 4) + 256;
+}
+
+A2AV_API int moe_combine_backward(int W, int64_t T, int k, int64_t H, const void *const *back,
+                                  const int64_t *const *perm, const float *const *weights,
+                                  const void *const *d_out, void *const *d_back,
+                                  float *const *d_weights, void *workspace,
+                                  size_t workspace_bytes, int32_t *status, hipStream_t stream) {
+    const size_t need = moe_combine_backward_workspace_bytes(W, T, k);
+    if (need == 0 || H < 1 || !back || !perm || !weights || !d_out || !d_back || !d_weights ||
+        !status)
+        return A2AV_EARG;
+    if ((uint64_t)H > (uint64_t)INT64_MAX / 2 ||
+        (uint64_t)T * (uint64_t)k > (uint64_t)INT64_MAX / (2 * (uint64_t)H))
+        return A2AV_EARG;
+    if (!workspace || workspace_bytes < need) return A2AV_EARG;
+    CombineGradArgs a;
+    std::memset(&a, 0, sizeof(a));
+    bool aligned = (H % 8) == 0;
+    for (int r = 0; r < W; r++) {
+        if (T > 0 && (!back[r] || !perm[r] || !weights[r] || !d_out[r] || !d_back[r] || !d_weights[r]))
+            return A2AV_EARG;
+        a.rows[r] = (const unsigned char *)back[r];
+        a.perm[r] = perm[r];
+        a.w[r] = weights[r];
+        a.d_out[r] = (const unsigned char *)d_out[r];
+        a.d_rows[r] = (unsigned char *)d_back[r];
+        a.d_w[r] = d_weights[r];
+        aligned = aligned && ((uintptr_t)back[r] % 16 == 0) && ((uintptr_t)d_out[r] % 16 == 0) &&
+                  ((uintptr_t)d_back[r] % 16 == 0);
+    }
+    a.mark = (int32_t *)workspace;
+    a.status = status;
+    a.T = T;
+    a.H = H;
+    a.k = k;
+    a.W = W;
+    if (T == 0) return A2AV_OK;
+    const dim3 slots((unsigned)((T * k + 255) / 256), W);
+    hipLaunchKernelGGL(k_perm_mark, slots, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(k_mark_check<false>, slots, dim3(256), 0, stream, a);
+    launch_combine_backward<false>(a, aligned, stream);
+    return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
+}
+
+A2AV_API size_t moe_combine_return_backward_workspace_bytes(int W, int64_t T, int k, int E) {
+    const size_t plan = moe_combine_return_workspace_bytes(W, T, k, E);
+    const size_t mark = moe_combine_backward_workspace_bytes(W, T, k);
+    return plan == 0 || mark == 0 ? 0 : plan + mark;
+}
+
+A2AV_API int moe_combine_return_backward(int W, int64_t T, int k, int E, int64_t H,
+                                         const int64_t *expert_counts, const int32_t *const *ids,
+                                         const int64_t *const *perm, const void *const *recv,
+                                         const int64_t *recv_rows, const float *const *weights,
+                                         const void *const *d_out, void *const *d_recv,
+                                         float *const *d_weights, int layout, void *workspace,
+                                         size_t workspace_bytes, int32_t *status,
+                                         hipStream_t stream) {
+    const size_t need = moe_combine_return_backward_workspace_bytes(W, T, k, E);
+    if (need == 0 || H < 1 || !expert_counts || !ids || !perm || !recv || !recv_rows || !weights ||
+        !d_out || !d_recv || !d_weights || !status || (layout != 0 && layout != 1))
+        return A2AV_EARG;
+    if ((uint64_t)H > (uint64_t)INT64_MAX / 2) return A2AV_EARG;
+    const uint64_t row_bytes = 2 * (uint64_t)H;
+    if ((uint64_t)T * (uint64_t)k > (uint64_t)INT64_MAX / row_bytes) return A2AV_EARG;
+    if (!workspace || workspace_bytes < need) return A2AV_EARG;
+    ShiftArgs p;
+    ReturnArgs c;
+    CombineGradArgs a;
+    std::memset(&p, 0, sizeof(p));
+    std::memset(&c, 0, sizeof(c));
+    std::memset(&a, 0, sizeof(a));
+    bool aligned = (H % 8) == 0;
+    for (int r = 0; r < W; r++) {
+        if (T > 0 && (!ids[r] || !perm[r] || !weights[r] || !d_out[r] || !d_weights[r]))
+            return A2AV_EARG;
+        const int64_t rows = recv_rows[r];
+        if (rows < 0 || (uint64_t)rows > (uint64_t)INT64_MAX / row_bytes) return A2AV_EARG;
+        if (rows > 0 && (!recv[r] || !d_recv[r])) return A2AV_EARG;
+        p.base[r] = (const unsigned char *)recv[r];
+        p.limit[r] = rows;
+        c.ids[r] = ids[r];
+        c.perm[r] = perm[r];
+        a.rows[r] = (const unsigned char *)recv[r];
+        a.perm[r] = perm[r];
+        a.w[r] = weights[r];
+        a.d_out[r] = (const unsigned char *)d_out[r];
+        a.d_rows[r] = (unsigned char *)d_recv[r];
+        a.d_w[r] = d_weights[r];
+        a.ids[r] = ids[r];
+        aligned = aligned && ((uintptr_t)recv[r] % 16 == 0) && ((uintptr_t)d_out[r] % 16 == 0) &&
+                  ((uintptr_t)d_recv[r] % 16 == 0);
+    }
+    unsigned char *ws = (unsigned char *)workspace;
+    const size_t table = round256((size_t)W * (size_t)E * 8);
+    const size_t plan = moe_combine_return_workspace_bytes(W, T, k, E);
+    uint64_t *row_addr = (uint64_t *)ws;
+    int64_t *ystart = (int64_t *)(ws + table);
+    int32_t *words = (int32_t *)(ws + 2 * table);
+    uint64_t *xaddr = (uint64_t *)(ws + 2 * table + 256);
+    p.counts = expert_counts;
+    p.row_addr = row_addr;
+    p.ystart = ystart;
+    p.words = words;
+    p.status = status;
+    p.R = row_bytes;
+    p.W = W;
+    p.E = E;
+    p.layout = layout;
+    p.over_bit = A2AV_ST_SEND_OVERRUN;
+    p.check_counts = 1;
+    c.counts = expert_counts;
+    c.row_addr = row_addr;
+    c.ystart = ystart;
+    c.xaddr = xaddr;
+    c.mark = (int32_t *)(ws + plan);
+    c.words = words;
+    c.status = status;
+    c.R = row_bytes;
+    c.Q = T * k;
+    c.E = E;
+    c.W = W;
+    a.mark = c.mark;
+    a.xaddr = xaddr;
+    a.words = words;
+    a.status = status;
+    a.T = T;
+    a.H = H;
+    a.k = k;
+    a.W = W;
+    a.P = E / W;
+    hipLaunchKernelGGL(k_shift_plan, dim3(W), dim3(kPlanThreads), 0, stream, p);
+    if (c.Q > 0) {
+        const dim3 slots((unsigned)((c.Q + 255) / 256), W);
+        hipLaunchKernelGGL(k_slot_check, slots, dim3(256), 0, stream, c);
+        hipLaunchKernelGGL(k_mark_check<true>, slots, dim3(256), 0, stream, a);
+    }
+    launch_combine_backward<true>(a, aligned, stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

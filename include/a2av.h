@@ -71,8 +71,10 @@ extern "C" {
 #define A2AV_ST_SEND_OVERRUN 2   /* a rank sends more rows than in_rows        */
 #define A2AV_ST_RECV_OVERFLOW 4  /* a rank receives more rows than out_cap_rows */
 #define A2AV_ST_BAD_EXPERT 8     /* an expert id is outside [0, E)              */
-#define A2AV_ST_BAD_OFFSETS 16   /* offsets are not the exclusive scans of S    */
-#define A2AV_ST_BAD_PERM 32      /* a permutation entry is outside [0, T*k)     */
+#define A2AV_ST_BAD_OFFSETS 16   /* offsets are not the exclusive scans of S, or
+                                    expert offsets that descend               */
+#define A2AV_ST_BAD_PERM 32      /* a permutation entry is outside [0, T*k), or
+                                    given twice where rows are written        */
 
 /* ABI version of the loaded library (A2AV_ABI_VERSION it was built with). */
 int a2av_abi_version(void);
@@ -485,6 +487,226 @@ int moe_combine_grouped(int W, int64_t T, int k, int E, int64_t H, const int64_t
                         const void *const *expert_side, const int64_t *exp_rows,
                         const float *const *weights, void *const *out, void *workspace,
                         size_t workspace_bytes, int32_t *status, hipStream_t stream);
+
+/* element types of router logits and expert rows */
+#define A2AV_DT_F32 0
+#define A2AV_DT_BF16 1
+#define A2AV_DT_F16 2
+
+/* scores of moe_route */
+#define A2AV_SCORE_SOFTMAX 0
+#define A2AV_SCORE_SIGMOID 1
+
+/* activations of moe_expert_linear */
+#define A2AV_ACT_NONE 0
+#define A2AV_ACT_RELU 1
+#define A2AV_ACT_GELU 2   /* x * Phi(x), Phi the normal distribution function */
+#define A2AV_ACT_SILU 3   /* x * sigmoid(x) */
+#define A2AV_ACT_SWIGLU 4 /* silu(gate) * up, two products of N columns each  */
+
+/* widest row of moe_expert_linear */
+#define A2AV_MAX_WIDTH (1 << 20)
+
+/*
+ * The router in front of moe_pack and moe_pack_dispatch, for all W ranks: the
+ * expert ids and gate weights of every token from its E logits z.
+ *   s[e]  = softmax(z)[e] or sigmoid(z[e])          (score)
+ *   c[e]  = s[e] + bias[e]                          (bias may be NULL: 0)
+ * With groups > 1 the experts form `groups` blocks of E/groups; a group's
+ * score is the sum of its group_top largest c, and only the topk_groups best
+ * groups (ties: lowest group) keep their experts. The k largest c of those,
+ * in descending order, are the ids. c and the group scores are compared as
+ * evaluated in double; of equal c the larger logit comes first, then the
+ * lowest id. The bias (of a load balancer) only selects:
+ *   weights[j] = scale * s[id_j]                          (renorm 0)
+ *   weights[j] = scale * s[id_j] / sum_i s[id_i], or 0 if that sum is 0  (1)
+ *   k, E           1 <= k <= min(64, topk_groups * E / groups),
+ *                  E <= A2AV_MAX_EXPERTS (E % W is not asked for here)
+ *   groups         divides E, at most 64; 1 <= topk_groups <= groups;
+ *                  group_top 1 or 2, at most E / groups
+ *   logits[W]      device [T][E] of type (A2AV_DT_*) per rank
+ *   bias           device fp32 [E] or NULL, shared by the ranks
+ *   ids[W]         device int32 [T][k] per rank, written (moe_pack's ids)
+ *   weights[W]     device fp32 [T][k] per rank, written (moe_combine's)
+ * A logit of -inf masks its expert: its score is 0 and its c is -inf, so it
+ * is chosen (with weight 0) only when nothing else is left; in a row whose
+ * logits are all -inf the first k experts are chosen, with weight 0, from the
+ * groups kept by the same rule. A c that is NaN counts as -inf. A token with
+ * a NaN among its logits, or +inf under softmax, gets the ids 0..k-1 and NaN
+ * weights. Nothing is reported in status.
+ * One kernel.
+ */
+int moe_route(int W, int64_t T, int k, int E, int type, int score,
+              const void *const *logits, const float *bias, int groups, int topk_groups,
+              int group_top, int renorm, float scale, int32_t *const *ids,
+              float *const *weights, int32_t *status, hipStream_t stream);
+
+/*
+ * The gradient of moe_route's weights in its logits, the ids held fixed
+ * (the bias and the grouping only select and have no gradient). With
+ * g_j = scale * d_weights[j] and s_j = s[id_j]:
+ *   renorm 1:  ds_j = (g_j - sum_i g_i s_i / S) / S, S = sum_i s_i
+ *   renorm 0:  ds_j = g_j
+ *   softmax:   d_logits[e] = s[e] * (sum_{j: id_j = e} ds_j - sum_j ds_j s_j)
+ *   sigmoid:   d_logits[e] = s[e] * (1 - s[e]) * sum_{j: id_j = e} ds_j
+ *   logits[W], ids[W], weights[W]   moe_route's input and outputs; the
+ *                  weights stand for the s_j above (with renorm and softmax
+ *                  no logit is read), so all-zero weights have zero gradients
+ *   d_weights[W]   device fp32 [T][k]
+ *   d_logits[W]    device [T][E] of type, every element written
+ *   status         A2AV_ST_BAD_EXPERT for an id outside [0, E): nothing is
+ *                  written.
+ * Ids may repeat (their gradients add up). A token with NaN weights gets NaN
+ * for its chosen experts.
+ * Two kernels: a range check of the ids, then the gradient.
+ */
+int moe_route_backward(int W, int64_t T, int k, int E, int type, int score,
+                       const void *const *logits, const int32_t *const *ids,
+                       const float *const *weights, int renorm, float scale,
+                       const float *const *d_weights, void *const *d_logits, int32_t *status,
+                       hipStream_t stream);
+
+/*
+ * Workspace bytes moe_combine_backward needs (0 for invalid sizes).
+ */
+size_t moe_combine_backward_workspace_bytes(int W, int64_t T, int k);
+
+/*
+ * The gradient of moe_combine, in its rows and its weights: for every rank r
+ * and slot q = t*k + j,
+ *   d_back[r][perm[r][q]][h] = weights[r][q] * d_out[r][t][h]  (fp32, rounded
+ *                              once to bf16, NaN as 0x7FC0)
+ *   d_weights[r][q] = sum_h back[r][perm[r][q]][h] * d_out[r][t][h]
+ *                              (products and sums in fp32, in a fixed order)
+ *   back[W], perm[W], weights[W]  as moe_combine
+ *   d_out[W]      device bf16 [T][H] per rank, the gradient of its out
+ *   d_back[W]     device bf16 [T*k][H] per rank, written
+ *   d_weights[W]  device fp32 [T][k] per rank, written
+ *   workspace     device scratch of >= moe_combine_backward_workspace_bytes()
+ *   status        A2AV_ST_BAD_PERM if a perm entry is outside [0, T*k) or
+ *                 appears twice (two slots would write one row): nothing but
+ *                 the workspace is written.
+ * Three kernels: every slot marks its row, every slot checks its mark, then
+ * the gradient (one workgroup per token, its waves taking the slots in turn).
+ */
+int moe_combine_backward(int W, int64_t T, int k, int64_t H, const void *const *back,
+                         const int64_t *const *perm, const float *const *weights,
+                         const void *const *d_out, void *const *d_back, float *const *d_weights,
+                         void *workspace, size_t workspace_bytes, int32_t *status,
+                         hipStream_t stream);
+
+/*
+ * Workspace bytes moe_combine_return_backward needs (0 for invalid sizes).
+ */
+size_t moe_combine_return_backward_workspace_bytes(int W, int64_t T, int k, int E);
+
+/*
+ * The gradient of moe_combine_return (layout 1: also of moe_combine_grouped):
+ * moe_combine_backward with every row read, and its gradient written, at the
+ * owner of its expert, where moe_pack_dispatch left it.
+ *   expert_counts, ids[W], perm[W], recv[W], recv_rows[W], weights[W], layout
+ *                 as moe_combine_return
+ *   d_out[W]      device bf16 [T][H] per source
+ *   d_recv[W]     device bf16 [recv_rows[d]][H] per owner, written in the
+ *                 rows that slots have; rows past the owner's total untouched
+ *   d_weights[W]  device fp32 [T][k] per source, written
+ *   workspace     device scratch of at least
+ *                 moe_combine_return_backward_workspace_bytes()
+ *   status        as moe_unpack_return, and A2AV_ST_BAD_PERM for a perm entry
+ *                 that appears twice; nothing but the workspace is written on
+ *                 failure.
+ * The gradient of the tokens behind moe_pack_dispatch is the sum of their
+ * slots' rows: moe_combine_return over the rows' gradients with weights of 1.
+ * Four kernels: the plan of moe_pack_dispatch, a check of every slot that
+ * also records its row's address and marks it, the check of the marks, and
+ * the gradient.
+ */
+int moe_combine_return_backward(int W, int64_t T, int k, int E, int64_t H,
+                                const int64_t *expert_counts, const int32_t *const *ids,
+                                const int64_t *const *perm, const void *const *recv,
+                                const int64_t *recv_rows, const float *const *weights,
+                                const void *const *d_out, void *const *d_recv,
+                                float *const *d_weights, int layout, void *workspace,
+                                size_t workspace_bytes, int32_t *status, hipStream_t stream);
+
+/*
+ * Workspace bytes moe_expert_linear needs (0 for invalid sizes): x_rows as
+ * below (host).
+ */
+size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int act,
+                                         const int64_t *x_rows);
+
+/*
+ * The experts' products on the rows that moe_pack_dispatch (layout 1),
+ * moe_dispatch_grouped or moe_regroup delivered, for all W ranks: rank d owns
+ * P experts, expert j's rows are expert_offsets[d][j] .. [j+1] of x[d], and
+ *   h = x[d][row] . weight[d][j]^T + bias[d][j]     (fp32 sums)
+ *   out[d][row] = act(h) + residual[d][row]         (fp32, rounded once)
+ *   pre[d][row] = h                                 (rounded once)
+ * With A2AV_ACT_SWIGLU the weight has 2N rows, the N gate rows and then the N
+ * up rows, and act(h) = silu(h[0..N)) * h[N..2N). NW below is 2N then, else N.
+ *   K, N            1 .. A2AV_MAX_WIDTH
+ *   type            A2AV_DT_BF16 or A2AV_DT_F16, of every array
+ *   x[W]            device [x_rows[d]][K] (host x_rows)
+ *   expert_offsets  device int64 [W][P+1] (block_offsets / expert_offsets of
+ *                   the calls above); W * P <= A2AV_MAX_EXPERTS
+ *   weight[W]       device [P][NW][K]
+ *   bias            host array of W device [P][NW], or NULL
+ *   residual        host array of W device [x_rows[d]][N], or NULL; may be out
+ *   out[W]          device [x_rows[d]][N], written below the rank's total
+ *   pre             host array of W device [x_rows[d]][NW], written below the
+ *                   rank's total (what the backward pass needs), or NULL
+ *   workspace       device scratch of >= moe_expert_linear_workspace_bytes()
+ *   status          A2AV_ST_BAD_OFFSETS (a rank's offsets do not start at 0 or
+ *                   descend), A2AV_ST_SEND_OVERRUN (a total above x_rows):
+ *                   nothing but the workspace is written.
+ * Two kernels: a plan that checks the offsets and lists the row tiles of all
+ * experts, and the products on matrix cores. Sizes and alignments of any kind
+ * are accepted; rows that are 16-byte multiples at 16-byte-aligned bases take
+ * the fast path.
+ */
+int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int act,
+                      const void *const *x, const int64_t *x_rows,
+                      const int64_t *expert_offsets, const void *const *weight,
+                      const void *const *bias, const void *const *residual, void *const *out,
+                      void *const *pre, void *workspace, size_t workspace_bytes,
+                      int32_t *status, hipStream_t stream);
+
+/*
+ * Workspace bytes moe_expert_linear_backward needs (0 for invalid sizes).
+ */
+size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64_t N, int act,
+                                                  const int64_t *x_rows);
+
+/*
+ * The gradient of moe_expert_linear from d_out, that of its out (which is
+ * also the residual's):
+ *   d_pre    = d_out * act'(pre)      (fp32, rounded once to type)
+ *   d_x      = d_pre . weight[d][j]   (fp32 sums, rounded once)
+ *   d_weight = d_pre^T . x            (over the expert's rows; 0 if it has none)
+ *   d_bias   = sum of d_pre           (over the expert's rows, before d_pre's
+ *                                      rounding, in a fixed order)
+ * The products read the rounded d_pre, as they would between two layers.
+ *   x, x_rows, expert_offsets, weight, type, act   as moe_expert_linear
+ *   pre, d_pre     host arrays of W device [x_rows[d]][NW]; both NULL with
+ *                  A2AV_ACT_NONE, where d_pre is d_out
+ *   d_out[W]       device [x_rows[d]][N]
+ *   d_x            host array of W device [x_rows[d]][K], or NULL: not wanted
+ *   d_weight       host array of W device [P][NW][K], or NULL: not wanted
+ *   d_bias         host array of W device [P][NW], or NULL: not wanted
+ *   workspace      device scratch of >= ..._backward_workspace_bytes()
+ *   status         as moe_expert_linear
+ * Rows past a rank's total are not read, and untouched in d_pre and d_x.
+ * One kernel each for the plan, d_pre (with the bias sums of row blocks), the
+ * bias, d_x and d_weight, less what is not wanted.
+ */
+int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int type, int act,
+                               const void *const *x, const int64_t *x_rows,
+                               const int64_t *expert_offsets, const void *const *weight,
+                               const void *const *pre, const void *const *d_out,
+                               void *const *d_pre, void *const *d_x, void *const *d_weight,
+                               void *const *d_bias, void *workspace, size_t workspace_bytes,
+                               int32_t *status, hipStream_t stream);
 
 /*
  * Workspace bytes keys_bucketize needs (0 for invalid sizes).

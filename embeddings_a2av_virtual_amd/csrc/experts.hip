@@ -8,6 +8,7 @@
 //   d_weight   d_pre^T . x                             contraction over rows
 //
 //   k_expert_plan   checks the offsets, lists the row tiles of all experts
+//   k_expert_tile   one tile of one product, 16-byte rows
 //   k_expert_any    one 64 x 64 tile of one product, any size and alignment
 //   k_expert_dpre   d_pre = d_out * act'(pre), with the bias sums of row blocks
 //   k_expert_dbias  the bias sums of an expert's row blocks, in order
@@ -166,7 +167,6 @@ struct ExpertArgs {
     int W, P;
     int act;
     int has_bias, has_residual, has_pre;
-    int tile_rows;
 };
 
 // The weight row behind column c of the product: with SwiGLU, blocks of 16
@@ -306,7 +306,326 @@ __global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
         }
 }
 
+// ------------------------------------------------------------------ the fast products
+// Tiles of BM rows and BC columns, a contraction step of 64, both operands
+// through LDS in two stages that buffer loads fill directly: while the matrix
+// cores work on one stage the other's loads are in flight, and one barrier a
+// step both publishes a stage and frees the other. An operand comes in one of
+// two forms, by what its memory holds contiguously:
+//   along the contraction (x and weight forward, d_pre for d_x): LDS rows of
+//     64 elements, the eight 16-byte chunks of row r permuted by r % 8, read
+//     as 16-byte fragments;
+//   along the tile's rows or columns (the others): LDS rows are contraction
+//     steps of BM or BC elements, 32-byte units permuted by the row, read with
+//     the transposing LDS load (4 contraction steps x 16 columns a group).
+// Both permutations put the lanes of one LDS access in different banks.
+// Rows, columns and contraction steps outside are loaded out of the buffer's
+// range, which writes zeros to LDS.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kStep = 64;                     // contraction elements a step
+constexpr uint32_t kOutside = 0x80000000u;    // a byte offset past every buffer
+
+__device__ __forceinline__ rsrc_t buffer(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)bytes, 0x00020000);
+}
+
+// The 32-byte unit of LDS row r that holds unit 0 of a contraction-major
+// operand with COLS columns is the one at this number; the others by xor.
+template <int COLS>
+__device__ __forceinline__ int unit_shift(int r) {
+    if constexpr (COLS == 256) return (r & 3) | (((r >> 3) & 3) << 2);
+    else if constexpr (COLS == 128) return (r & 3) | (((r >> 3) & 1) << 2);
+    else return ((r >> 1) & 1) | (((r >> 3) & 1) << 1);
+}
+
+// One operand of a tile: where its elements are and how they reach LDS.
+// ROWS: tile rows (or columns); MAJOR: contiguous along the contraction.
+template <int ROWS, int THREADS, bool MAJOR>
+struct Operand {
+    static constexpr int kLoads = ROWS * 8 / THREADS;  // 16-byte loads a thread and step
+    static constexpr int kWaves = THREADS / kWave;
+    const unsigned char *base;   // MAJOR: row 0 of the tile; else contraction step 0, column 0
+    const unsigned char *base2;  // the up rows of a gated product
+    uint32_t span, span2;        // MAJOR: bytes of the tile's rows
+    uint32_t off[kLoads];
+    int64_t stride;              // bytes of a memory row
+    int64_t len;                 // contraction length
+    int k;                       // MAJOR: this lane's element of a step
+
+    // MAJOR: `rows` rows from p, ld elements wide, all of them contraction.
+    // A gated product takes blocks of 16 rows from p and p2 in turn.
+    __device__ __forceinline__ void along(const uint16_t *p, const uint16_t *p2, int64_t ld, int64_t rows,
+                                          int wave, int lane) {
+        const int64_t most = p2 ? ROWS / 2 : ROWS;
+        base = (const unsigned char *)p;
+        base2 = (const unsigned char *)p2;
+        stride = ld * 2;
+        len = ld;
+        span = (uint32_t)((rows < most ? rows : most) * stride);
+        k = ((lane & 7) ^ (lane >> 3)) * 8;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int r = (i * kWaves + wave) * 8;
+            const int row = (p2 ? (r >> 5) * 16 + (r & 8) : r) + (lane >> 3);
+            off[i] = (uint32_t)(row * stride) + k * 2;
+        }
+    }
+    // Not MAJOR: `steps` memory rows of ld elements from p, columns c0 .. of cols.
+    __device__ __forceinline__ void across(const uint16_t *p, int64_t ld, int64_t steps, int64_t c0, int64_t cols,
+                                           int wave, int lane) {
+        constexpr int kPer = ROWS / 8;             // lanes a memory row
+        base = (const unsigned char *)(p + c0);
+        stride = ld * 2;
+        len = steps;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int row = (i * kWaves + wave) * (kWave / kPer) + lane / kPer, at = lane % kPer;
+            const int c = ((((at >> 1) ^ unit_shift<ROWS>(row)) << 1) | (at & 1)) * 8;
+            off[i] = c0 + c < cols ? (uint32_t)(row * stride) + c * 2 : kOutside;
+        }
+    }
+    // Loads of contraction step s into an LDS stage; rows at or past `most` of
+    // a MAJOR operand are not needed.
+    template <int MOST>
+    __device__ __forceinline__ void load(uint16_t *lds, int64_t s, int wave, bool gated) const {
+        if constexpr (MAJOR) {
+            const int64_t left = len - s * kStep;
+            const uint32_t out = k < left ? 0 : kOutside;
+#pragma unroll
+            for (int i = 0; i < kLoads; i++) {
+                if (i * kWaves * 8 >= MOST) break;
+                const int r = (i * kWaves + wave) * 8;
+                const unsigned char *p = gated && ((r >> 4) & 1) ? base2 : base;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p, span), (lds_void *)(lds + r * kStep), 16,
+                                                         (int)(off[i] | out), (int)(s * kStep * 2), 0, 0);
+            }
+        } else {
+            const int64_t left = len - s * kStep;
+            const rsrc_t b = buffer(base + s * kStep * stride, (uint32_t)((left < kStep ? left : kStep) * stride));
+#pragma unroll
+            for (int i = 0; i < kLoads; i++)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    b, (lds_void *)(lds + (i * kWaves + wave) * (kWave * 8)), 16, (int)off[i], 0, 0, 0);
+        }
+    }
+};
+
+// The 16 x 32 fragment at tile row `row` (a multiple of 16) and half kk of a
+// step, from an LDS stage.
+template <typename T, int ROWS, bool MAJOR>
+__device__ __forceinline__ typename T::frag fragment(const uint16_t *lds, int row, int kk, int lane) {
+    if constexpr (MAJOR) {
+        const int at = (row + (lane & 15)) * kStep + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) << 3);
+        return *(const typename T::frag *)(lds + at);
+    } else {
+        const int r = kk * 32 + (lane >> 4) * 8 + ((lane >> 2) & 3);
+        const int at = r * ROWS + (((row >> 4) ^ unit_shift<ROWS>(r)) << 4) + (lane & 3) * 4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 4 * ROWS));
+        return __builtin_bit_cast(typename T::frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+}
+
+template <int KIND, int BM, int BC, int WM, int WC>
+struct Shape {
+    static constexpr int kThreads = WM * WC * kWave;
+    static constexpr bool kMajorA = KIND != kDweight, kMajorB = KIND == kForward;
+    static constexpr int kBlocksM = BM / WM / 16, kBlocksC = BC / WC / 16;
+    typedef Operand<BM, kThreads, kMajorA> A;
+    typedef Operand<BC, kThreads, kMajorB> B;
+};
+
+// The contraction of one tile with NB row blocks a wave: the blocks of the
+// waves alternate, so that a tile with few rows keeps all of them busy.
+template <int KIND, typename T, int BM, int BC, int WM, int WC, int NB>
+__device__ __forceinline__ void contract(const typename Shape<KIND, BM, BC, WM, WC>::A &oa,
+                                         const typename Shape<KIND, BM, BC, WM, WC>::B &ob, uint16_t *sa0,
+                                         uint16_t *sb0, uint16_t *sa1, uint16_t *sb1, bool gated,
+                                         f32x4 (&acc)[Shape<KIND, BM, BC, WM, WC>::kBlocksM]
+                                                     [Shape<KIND, BM, BC, WM, WC>::kBlocksC]) {
+    typedef Shape<KIND, BM, BC, WM, WC> S;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WC, wc = wave % WC;
+    const int64_t steps = (oa.len + kStep - 1) / kStep;
+    const auto work = [&](const uint16_t *sa, const uint16_t *sb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            typename T::frag fb[S::kBlocksC], fa[NB];
+#pragma unroll
+            for (int c = 0; c < S::kBlocksC; c++)
+                fb[c] = fragment<T, BC, S::kMajorB>(sb, (wc * S::kBlocksC + c) * 16, kk, lane);
+#pragma unroll
+            for (int m = 0; m < NB; m++) fa[m] = fragment<T, BM, S::kMajorA>(sa, (m * WM + wm) * 16, kk, lane);
+#pragma unroll
+            for (int m = 0; m < NB; m++)
+#pragma unroll
+                for (int c = 0; c < S::kBlocksC; c++) acc[m][c] = T::mfma(fb[c], fa[m], acc[m][c]);
+        }
+    };
+    if (steps == 0) return;  // an expert without rows: its d_weight is 0
+    oa.template load<NB * WM * 16>(sa0, 0, wave, false);
+    ob.template load<BC>(sb0, 0, wave, gated);
+    for (int64_t s = 0; s < steps; s += 2) {
+        __syncthreads();
+        if (s + 1 < steps) {
+            oa.template load<NB * WM * 16>(sa1, s + 1, wave, false);
+            ob.template load<BC>(sb1, s + 1, wave, gated);
+        }
+        work(sa0, sb0);
+        if (s + 1 < steps) {
+            __syncthreads();
+            if (s + 2 < steps) {
+                oa.template load<NB * WM * 16>(sa0, s + 2, wave, false);
+                ob.template load<BC>(sb0, s + 2, wave, gated);
+            }
+            work(sa1, sb1);
+        }
+    }
+}
+
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+// Eight neighbouring elements: added to y, and y rounded into them.
+template <typename T>
+__device__ __forceinline__ void add8(float (&y)[8], const uint16_t *p) {
+    const u16x8 v = *(const u16x8 *)p;
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] += T::to_float(v[i]);
+}
+template <typename T>
+__device__ __forceinline__ void put8(uint16_t *p, const float (&y)[8]) {
+    u16x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = T::from_float(y[i]);
+    *(u16x8 *)p = v;
+}
+
+template <int KIND, typename T, int BM, int BC, int WM, int WC>
+__global__ __launch_bounds__(WM *WC *kWave) void k_expert_tile(const ExpertArgs a) {
+    typedef Shape<KIND, BM, BC, WM, WC> S;
+    __shared__ __align__(16) uint16_t sa0[BM * kStep], sa1[BM * kStep], sb0[BC * kStep], sb1[BC * kStep];
+    if (status_at_entry(a.status)) return;
+    int e, mt;
+    if constexpr (KIND == kDweight) {
+        e = blockIdx.z;
+        mt = blockIdx.y;
+    } else {
+        const int t = blockIdx.y + gridDim.y * blockIdx.z;
+        if (t >= a.tiles[0]) return;
+        e = a.tiles[2 + 2 * t];
+        mt = a.tiles[3 + 2 * t];
+    }
+    const int d = e / a.P, j = e - d * a.P;
+    const int64_t row0 = a.offsets[(int64_t)d * (a.P + 1) + j];
+    const int64_t rows = a.offsets[(int64_t)d * (a.P + 1) + j + 1] - row0;
+    const bool glu = KIND == kForward && a.act == A2AV_ACT_SWIGLU;
+    const int64_t M = KIND == kDweight ? a.NW : rows;
+    const int64_t C = KIND == kForward ? (glu ? (a.N + 15) / 16 * 32 : a.N) : a.K;
+    const int64_t m0 = (int64_t)mt * BM, c0 = (int64_t)blockIdx.x * BC;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WC, wc = wave % WC;
+    typename S::A oa;
+    typename S::B ob;
+    const uint16_t *pa = (const uint16_t *)a.a[d], *pb = (const uint16_t *)a.b[d];
+    if constexpr (KIND == kForward) {
+        oa.along(pa + (row0 + m0) * a.K, nullptr, a.K, M - m0, wave, lane);
+        const uint16_t *w = pb + (int64_t)j * a.NW * a.K;
+        const int64_t n0 = glu ? c0 / 2 : c0;
+        ob.along(w + n0 * a.K, glu ? w + (a.N + n0) * a.K : nullptr, a.K, a.N - n0, wave, lane);
+    } else if constexpr (KIND == kDx) {
+        oa.along(pa + (row0 + m0) * a.NW, nullptr, a.NW, M - m0, wave, lane);
+        ob.across(pb + (int64_t)j * a.NW * a.K, a.K, a.NW, c0, C, wave, lane);
+    } else {
+        oa.across(pa + row0 * a.NW, a.NW, rows, m0, M, wave, lane);
+        ob.across(pb + row0 * a.K, a.K, rows, c0, C, wave, lane);
+    }
+    f32x4 acc[S::kBlocksM][S::kBlocksC] = {};
+    const int64_t left = M - m0;
+    if (S::kBlocksM >= 8 && left <= WM * 16 * 2)
+        contract<KIND, T, BM, BC, WM, WC, 2>(oa, ob, sa0, sb0, sa1, sb1, glu, acc);
+    else if (S::kBlocksM >= 4 && left <= WM * 16 * (S::kBlocksM / 2))
+        contract<KIND, T, BM, BC, WM, WC, (S::kBlocksM >= 4 ? S::kBlocksM / 2 : 1)>(oa, ob, sa0, sb0, sa1, sb1, glu, acc);
+    else
+        contract<KIND, T, BM, BC, WM, WC, S::kBlocksM>(oa, ob, sa0, sb0, sa1, sb1, glu, acc);
+    // The sums leave through LDS, so that one lane gets 8 neighbouring columns
+    // of a row (16-byte stores, whole rows of the wave's columns at a time)
+    // and the epilogue's code exists once: in passes of kPass row blocks, each
+    // wave in its own part of the stages. A lane holds columns (lane / 16) * 4
+    // .. + 3 of row lane % 16 of each 16 x 16; the 16-byte chunks of a row are
+    // permuted by the row, which keeps both sides off each other's banks.
+    constexpr int kPass = S::kBlocksM < 4 ? S::kBlocksM : 4, kCols = S::kBlocksC * 16;
+    __syncthreads();
+    constexpr int kPerArray = WM * WC / 4;
+    uint16_t *part = wave / kPerArray == 0 ? sa0 : wave / kPerArray == 1 ? sa1 : wave / kPerArray == 2 ? sb0 : sb1;
+    f32x4 *sums = (f32x4 *)part + wave % kPerArray * (kPass * 16 * kCols / 4);
+#pragma unroll
+    for (int p = 0; p < S::kBlocksM / kPass; p++) {
+        if (p * kPass * WM * 16 >= left) break;
+#pragma unroll
+        for (int u = 0; u < kPass; u++)
+#pragma unroll
+            for (int v = 0; v < S::kBlocksC; v++)
+                sums[(u * 16 + (lane & 15)) * (kCols / 4) + ((v * 4 + (lane >> 4)) ^ (lane & (kCols / 4 - 1)))] =
+                    acc[p * kPass + u][v];
+        asm volatile("" ::: "memory");
+        const int per = glu ? kCols / 16 : kCols / 8;  // lanes a row
+        for (int r = lane / per; r < kPass * 16; r += kWave / per) {
+            const int64_t m = m0 + ((p * kPass + (r >> 4)) * WM + wm) * 16 + (r & 15);
+            const int q = lane % per;
+            if (m >= M) continue;
+            // gated: blocks of 16 gate and 16 up columns alternate
+            const int at = glu ? (q >> 1) * 8 + (q & 1) * 2 : q * 2;
+            const auto take = [&](int i, float(&y)[8]) {
+                const f32x4 lo = sums[r * (kCols / 4) + ((at + i) ^ (r & 15 & (kCols / 4 - 1)))];
+                const f32x4 hi = sums[r * (kCols / 4) + ((at + i + 1) ^ (r & 15 & (kCols / 4 - 1)))];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    y[c] = lo[c];
+                    y[c + 4] = hi[c];
+                }
+            };
+            float y[8];
+            take(0, y);
+            const int64_t c = c0 + wc * kCols;
+            if constexpr (KIND == kForward) {
+                const int64_t n = (glu ? c / 2 : c) + q * 8, row = row0 + m;
+                if (n >= a.N) continue;
+                const uint16_t *bias = (const uint16_t *)a.bias[d] + (int64_t)j * a.NW + n;
+                uint16_t *pre = (uint16_t *)a.pre[d] + row * a.NW + n;
+                if (a.has_bias) add8<T>(y, bias);
+                if (a.has_pre) put8<T>(pre, y);
+                if (glu) {
+                    float up[8];
+                    take(4, up);
+                    if (a.has_bias) add8<T>(up, bias + a.N);
+                    if (a.has_pre) put8<T>(pre + a.N, up);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) y[i] = y[i] * sigmoid(y[i]) * up[i];
+                } else if (a.act != A2AV_ACT_NONE) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) y[i] = act_of(a.act, y[i]);
+                }
+                if (a.has_residual) add8<T>(y, (const uint16_t *)a.residual[d] + row * a.N + n);
+                put8<T>((uint16_t *)a.out[d] + row * a.N + n, y);
+            } else {
+                if (c + q * 8 >= C) continue;
+                const int64_t row = KIND == kDx ? row0 + m : (int64_t)j * a.NW + m;
+                put8<T>((uint16_t *)a.out[d] + row * a.K + c + q * 8, y);
+            }
+        }
+        asm volatile("" ::: "memory");
+    }
+}
+
 // ------------------------------------------------------------------ d_pre and the bias
+constexpr int kBlockRows = 64;  // rows of a block of the bias sums
+
 struct DpreArgs {
     const void *pre[A2AV_MAX_W];
     const void *d_out[A2AV_MAX_W];
@@ -315,13 +634,13 @@ struct DpreArgs {
     const int64_t *offsets;
     const int32_t *tiles;
     const int32_t *first;
-    float *part;  // [tile][NW] bias sums of the row blocks
+    float *part;  // [tile][blocks][NW] bias sums of the row blocks
     const int32_t *status;
     int64_t N, NW;
     int W, P;
     int act;
     int has_bias;
-    int tile_rows;
+    int blocks;   // row blocks a tile
 };
 
 // One workgroup per (row block, 256 output columns): a thread walks its
@@ -329,15 +648,16 @@ struct DpreArgs {
 template <typename T>
 __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
     if (status_at_entry(a.status)) return;
-    const int t = blockIdx.y + gridDim.y * blockIdx.z;
+    const int64_t b = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+    const int t = (int)(b / a.blocks);
     if (t >= a.tiles[0]) return;
     const int e = a.tiles[2 + 2 * t], mt = a.tiles[3 + 2 * t];
     const int d = e / a.P, j = e - d * a.P;
     const int64_t *off = a.offsets + (int64_t)d * (a.P + 1) + j;
-    const int64_t r0 = off[0] + (int64_t)mt * a.tile_rows;
-    const int64_t r1 = r0 + a.tile_rows < off[1] ? r0 + a.tile_rows : off[1];
+    const int64_t r0 = off[0] + ((int64_t)mt * a.blocks + b % a.blocks) * kBlockRows;
+    const int64_t r1 = r0 + kBlockRows < off[1] ? r0 + kBlockRows : off[1];
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
+    if (n >= a.N || r0 >= r1) return;
     const bool glu = a.act == A2AV_ACT_SWIGLU;
     float s0 = 0.0f, s1 = 0.0f;
     for (int64_t r = r0; r < r1; r++) {
@@ -363,8 +683,8 @@ __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
         }
     }
     if (a.has_bias) {
-        a.part[(int64_t)t * a.NW + n] = s0;
-        if (glu) a.part[(int64_t)t * a.NW + a.N + n] = s1;
+        a.part[b * a.NW + n] = s0;
+        if (glu) a.part[b * a.NW + a.N + n] = s1;
     }
 }
 
@@ -374,14 +694,14 @@ __global__ __launch_bounds__(256) void k_expert_dbias(const DpreArgs a) {
     const int e = blockIdx.y, d = e / a.P, j = e - d * a.P;
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= a.NW) return;
+    const int64_t *off = a.offsets + (int64_t)d * (a.P + 1) + j;
+    const int64_t blocks = (off[1] - off[0] + kBlockRows - 1) / kBlockRows, b0 = (int64_t)a.first[e] * a.blocks;
     float s = 0.0f;
-    for (int t = a.first[e]; t < a.first[e + 1]; t++) s += a.part[(int64_t)t * a.NW + n];
+    for (int64_t b = 0; b < blocks; b++) s += a.part[(b0 + b) * a.NW + n];
     ((uint16_t *)a.d_bias[d])[(int64_t)j * a.NW + n] = T::from_float(s);
 }
 
 // ------------------------------------------------------------------ host
-constexpr int kBlockRows = 64;   // row blocks of the bias sums
-
 static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Row tiles of tile_rows that W * P experts with these rows can have, at most;
@@ -400,21 +720,41 @@ static int64_t tile_bound(int W, int P, int64_t K, int64_t N, int act, const int
     return t <= (1 << 30) ? t : -1;
 }
 
+// Tile shapes of the fast products, largest first.
+enum { kBig, kMid, kSmall };
+constexpr int kTile[] = {256, 128, 64};
+constexpr int kMostBlocks = 4;  // row blocks of the largest tile
+static_assert(kTile[kBig] == kMostBlocks * kBlockRows && kTile[kSmall] == kBlockRows && kAny == kBlockRows, "");
+
 struct Layout {
-    int64_t tiles;      // tile bound
+    int64_t tiles;      // most tiles, of the smallest size
     size_t first, part; // byte offsets
     size_t total;
 };
 
-static bool plan_layout(int W, int P, int64_t K, int64_t N, int act, const int64_t *x_rows,
-                        int tile_rows, bool with_part, Layout *l) {
-    l->tiles = tile_bound(W, P, K, N, act, x_rows, tile_rows);
+// The workspace holds the list of the smallest tiles, so that it does not
+// depend on the shape that a call takes.
+static bool plan_layout(int W, int P, int64_t K, int64_t N, int act, const int64_t *x_rows, bool with_part,
+                        Layout *l) {
+    l->tiles = tile_bound(W, P, K, N, act, x_rows, kBlockRows);
     if (l->tiles < 0) return false;
     l->first = round256((size_t)(l->tiles + 1) * 8);
     l->part = l->first + round256(((size_t)W * P + 1) * 4);
     const int64_t NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
-    l->total = l->part + (with_part ? round256((size_t)l->tiles * (size_t)NW * 4) : 0) + 256;
+    const size_t blocks = (size_t)l->tiles + (size_t)(kMostBlocks - 1) * W * P;
+    l->total = l->part + (with_part ? round256(blocks * (size_t)NW * 4) : 0) + 256;
     return true;
+}
+
+// The largest tile of which the product has enough to fill the compute units;
+// R rows over n experts, M x C the product of one of them (M = 0: its rows).
+static int shape_of(int64_t R, int64_t n, int64_t M, int64_t C) {
+    for (int s = kBig; s < kSmall; s++) {
+        const int64_t t = kTile[s], cols = (C + t - 1) / t;
+        const int64_t tiles = M ? n * ((M + t - 1) / t) : R <= n ? R : R / t + (R % (n * t) ? n / 2 : 0);
+        if (tiles * cols >= 200) return s;
+    }
+    return kSmall;
 }
 
 static void launch_plan(int W, int P, const int64_t *x_rows, const int64_t *offsets, int tile_rows,
@@ -438,18 +778,36 @@ static dim3 tile_grid(int64_t columns, int64_t tiles) {
     return dim3((unsigned)columns, (unsigned)y, (unsigned)((tiles + y - 1) / y));
 }
 
-template <int KIND>
-static void launch_product(const ExpertArgs &a, int type, int64_t tiles, hipStream_t stream) {
+template <int KIND, typename T>
+static void launch_product(const ExpertArgs &a, int shape, bool fast, int64_t tiles, hipStream_t stream) {
+    const int64_t cols = KIND != kForward ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
+    const int64_t t = fast ? kTile[shape] : kAny;
     dim3 g;
-    if (KIND == kDweight)
-        g = dim3((unsigned)((a.K + kAny - 1) / kAny), (unsigned)((a.NW + kAny - 1) / kAny), a.W * a.P);
-    else {
-        int64_t cols = KIND == kDx ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
-        g = tile_grid((cols + kAny - 1) / kAny, tiles);
-    }
-    if (type == A2AV_DT_BF16) hipLaunchKernelGGL((k_expert_any<KIND, Bf16>), g, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((k_expert_any<KIND, Fp16>), g, dim3(256), 0, stream, a);
+    if (KIND == kDweight) g = dim3((unsigned)((cols + t - 1) / t), (unsigned)((a.NW + t - 1) / t), a.W * a.P);
+    else g = tile_grid((cols + t - 1) / t, tiles);
+    if (!fast) hipLaunchKernelGGL((k_expert_any<KIND, T>), g, dim3(256), 0, stream, a);
+    else if (shape == kBig)
+        hipLaunchKernelGGL((k_expert_tile<KIND, T, 256, 256, 2, 4>), g, dim3(512), 0, stream, a);
+    else if (shape == kMid)
+        hipLaunchKernelGGL((k_expert_tile<KIND, T, 128, 128, 2, 2>), g, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_expert_tile<KIND, T, 64, 64, 2, 2>), g, dim3(256), 0, stream, a);
 }
+
+template <int KIND>
+static void launch_product(const ExpertArgs &a, int type, int shape, bool fast, int64_t tiles, hipStream_t stream) {
+    if (type == A2AV_DT_BF16) launch_product<KIND, Bf16>(a, shape, fast, tiles, stream);
+    else launch_product<KIND, Fp16>(a, shape, fast, tiles, stream);
+}
+
+// Most tiles of `rows` rows that a product's row tiles can be.
+static int64_t most_tiles(const int64_t *x_rows, int W, int P, int rows) {
+    int64_t total = 0;
+    for (int d = 0; d < W; d++) total += x_rows[d];
+    return total / rows + (int64_t)W * P;
+}
+
+static bool aligned16(const void *p) { return (uintptr_t)p % 16 == 0; }
 
 static bool fits(int64_t rows, int64_t width) {
     return (uint64_t)rows <= (uint64_t)INT64_MAX / 4 / (uint64_t)width;
@@ -462,7 +820,7 @@ using namespace a2av;
 A2AV_API size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int act,
                                                   const int64_t *x_rows) {
     Layout l;
-    return plan_layout(W, P, K, N, act, x_rows, kAny, false, &l) ? l.total : 0;
+    return plan_layout(W, P, K, N, act, x_rows, false, &l) ? l.total : 0;
 }
 
 A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int act,
@@ -472,7 +830,7 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
                                void *const *out, void *const *pre, void *workspace,
                                size_t workspace_bytes, int32_t *status, hipStream_t stream) {
     Layout l;
-    if (!plan_layout(W, P, K, N, act, x_rows, kAny, false, &l)) return A2AV_EARG;
+    if (!plan_layout(W, P, K, N, act, x_rows, false, &l)) return A2AV_EARG;
     if ((type != A2AV_DT_BF16 && type != A2AV_DT_F16) || !x || !expert_offsets || !weight || !out || !status)
         return A2AV_EARG;
     if (!workspace || (uintptr_t)workspace % 8 != 0 || workspace_bytes < l.total) return A2AV_EARG;
@@ -481,7 +839,10 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     a.K = K;
     a.N = N;
     a.NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
+    int64_t R = 0;
+    bool fast = K % 8 == 0 && N % 8 == 0;
     for (int d = 0; d < W; d++) {
+        R += x_rows[d];
         if (!fits(x_rows[d], K) || !fits(x_rows[d], a.NW)) return A2AV_EARG;
         if (!weight[d] || (bias && !bias[d])) return A2AV_EARG;
         if (x_rows[d] > 0 && (!x[d] || !out[d] || (residual && !residual[d]) || (pre && !pre[d])))
@@ -492,6 +853,8 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
         a.residual[d] = residual ? residual[d] : nullptr;
         a.out[d] = out[d];
         a.pre[d] = pre ? pre[d] : nullptr;
+        fast = fast && aligned16(a.a[d]) && aligned16(a.b[d]) && aligned16(a.bias[d]) && aligned16(a.residual[d]) &&
+               aligned16(a.out[d]) && aligned16(a.pre[d]);
     }
     a.offsets = expert_offsets;
     a.tiles = (const int32_t *)workspace;
@@ -502,15 +865,16 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     a.has_bias = bias != nullptr;
     a.has_residual = residual != nullptr;
     a.has_pre = pre != nullptr;
-    launch_plan(W, P, x_rows, expert_offsets, kAny, (unsigned char *)workspace, l, status, stream);
-    launch_product<kForward>(a, type, l.tiles, stream);
+    const int shape = fast ? shape_of(R, (int64_t)W * P, 0, a.NW) : kSmall;
+    launch_plan(W, P, x_rows, expert_offsets, kTile[shape], (unsigned char *)workspace, l, status, stream);
+    launch_product<kForward>(a, type, shape, fast, most_tiles(x_rows, W, P, kTile[shape]), stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }
 
 A2AV_API size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64_t N,
                                                            int act, const int64_t *x_rows) {
     Layout l;
-    return plan_layout(W, P, K, N, act, x_rows, kBlockRows, true, &l) ? l.total : 0;
+    return plan_layout(W, P, K, N, act, x_rows, true, &l) ? l.total : 0;
 }
 
 A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int type, int act,
@@ -522,7 +886,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
                                         size_t workspace_bytes, int32_t *status,
                                         hipStream_t stream) {
     Layout l;
-    if (!plan_layout(W, P, K, N, act, x_rows, kBlockRows, true, &l)) return A2AV_EARG;
+    if (!plan_layout(W, P, K, N, act, x_rows, true, &l)) return A2AV_EARG;
     const bool none = act == A2AV_ACT_NONE;
     if ((type != A2AV_DT_BF16 && type != A2AV_DT_F16) || !x || !expert_offsets || !weight || !d_out || !status)
         return A2AV_EARG;
@@ -547,8 +911,10 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
     g.first = (const int32_t *)(ws + l.first);
     g.part = (float *)(ws + l.part);
     g.has_bias = d_bias != nullptr;
-    g.tile_rows = kBlockRows;
+    int64_t R = 0;
+    bool fast = K % 8 == 0 && N % 8 == 0;
     for (int d = 0; d < W; d++) {
+        R += x_rows[d];
         if (!fits(x_rows[d], K) || !fits(x_rows[d], a.NW)) return A2AV_EARG;
         if (!weight[d] || (d_weight && !d_weight[d]) || (d_bias && !d_bias[d])) return A2AV_EARG;
         if (x_rows[d] > 0 && (!x[d] || !d_out[d] || (!none && (!pre[d] || !d_pre[d])) || (d_x && !d_x[d])))
@@ -562,10 +928,16 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         a.out[d] = d_x ? d_x[d] : nullptr;
         b.b[d] = x[d];
         b.out[d] = d_weight ? d_weight[d] : nullptr;
+        fast = fast && aligned16(a.a[d]) && aligned16(a.b[d]) && aligned16(a.out[d]) && aligned16(b.b[d]) &&
+               aligned16(b.out[d]);
     }
-    launch_plan(W, P, x_rows, expert_offsets, kBlockRows, ws, l, status, stream);
+    const int64_t n = (int64_t)W * P;
+    const int shape = fast ? shape_of(R, n, 0, K) : kSmall;
+    const int64_t tiles = most_tiles(x_rows, W, P, kTile[shape]);
+    g.blocks = kTile[shape] / kBlockRows;
+    launch_plan(W, P, x_rows, expert_offsets, kTile[shape], ws, l, status, stream);
     if (!none || d_bias) {
-        const dim3 grid = tile_grid((N + 255) / 256, l.tiles);
+        const dim3 grid = tile_grid((N + 255) / 256, tiles * g.blocks);
         if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dpre<Bf16>, grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL(k_expert_dpre<Fp16>, grid, dim3(256), 0, stream, g);
     }
@@ -574,7 +946,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dbias<Bf16>, grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL(k_expert_dbias<Fp16>, grid, dim3(256), 0, stream, g);
     }
-    if (d_x) launch_product<kDx>(a, type, l.tiles, stream);
-    if (d_weight) launch_product<kDweight>(b, type, l.tiles, stream);
+    if (d_x) launch_product<kDx>(a, type, shape, fast, tiles, stream);
+    if (d_weight) launch_product<kDweight>(b, type, fast ? shape_of(R, n, a.NW, K) : kSmall, fast, 0, stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

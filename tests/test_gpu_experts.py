@@ -211,6 +211,20 @@ def test_backward(shape, kind, act):
     Experts(per, K, N, kind, act, zlib.crc32(repr((shape, kind, act)).encode())).check_backward()
 
 
+# enough tiles of 256 x 256 and of 128 x 128 to fill the compute units
+LARGE = [([[257, 300, 30, 0, 512] + [260] * 35], 640, 648), ([[130] * 20, [1, 127] * 10], 200, 1000)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=["256", "128"])
+@pytest.mark.parametrize("kind,act", [("bf16", "swiglu"), ("fp16", "gelu"), ("fp16", "swiglu"), ("bf16", "none")])
+def test_large_tiles(shape, kind, act):
+    per, K, N = shape
+    seed = zlib.crc32(repr((shape, kind, act)).encode())
+    Experts(per, K, N, kind, act, seed).check_forward()
+    Experts(per, K, N, kind, act, seed, bias=False, residual=False, pre=False).check_forward()
+    Experts(per, K, N, kind, act, seed + 1).check_backward()
+
+
 @pytest.mark.parametrize("want", [("d_x",), ("d_weight",), ("d_bias",), ()], ids=str)
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_backward_of_some(want, act):

@@ -9,6 +9,7 @@
 //
 //   k_expert_plan   checks the offsets, lists the row tiles of all experts
 //   k_expert_tile   one tile of one product, 16-byte rows
+//   k_expert_few    16 columns of up to 16 rows, the weights read once
 //   k_expert_any    one 64 x 64 tile of one product, any size and alignment
 //   k_expert_dpre   d_pre = d_out * act'(pre), with the bias sums of row blocks
 //   k_expert_dbias  the bias sums of an expert's row blocks, in order
@@ -764,6 +765,104 @@ __global__ __launch_bounds__(WM *WC *kWave, STEP == 32 ? 4 : 2) void k_expert_ti
     }
 }
 
+// ------------------------------------------------------------------ few rows
+// Experts with a few rows each (decoded tokens): what has to move is the
+// weights, once, so they go from memory to the matrix cores' operands without
+// LDS. A workgroup has 16 output columns (gated: the 16 gate and the 16 up
+// rows behind them) of one tile of up to 16 rows; its four waves take blocks
+// of 128 contraction elements in turn, every load of two blocks in flight, and
+// their sums meet in LDS in wave order. Bound by the weights' bytes.
+constexpr int kFewRows = 16, kFewStep = 128;
+
+template <typename T>
+__device__ __forceinline__ typename T::frag load_frag(rsrc_t b, uint32_t off) {
+    return __builtin_bit_cast(typename T::frag, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+}
+
+template <typename T, bool GLU>
+__global__ __launch_bounds__(256) void k_expert_few(const ExpertArgs a) {
+    constexpr int kHalves = GLU ? 2 : 1;
+    __shared__ f32x4 sums[4][kHalves][kWave];
+    if (status_at_entry(a.status)) return;
+    const uint32_t t = blockIdx.x / (uint32_t)a.cols, ct = blockIdx.x - t * a.cols;
+    if ((int)t >= a.tiles[0]) return;
+    const int e = a.tiles[2 + 2 * t], mt = a.tiles[3 + 2 * t];
+    const int d = e / a.P, j = e - d * a.P;
+    const int64_t *ends = a.offsets + (int64_t)d * (a.P + 1) + j;
+    const int64_t row0 = ends[0] + (int64_t)mt * kFewRows, n0 = (int64_t)ct * 16;
+    const int rows = (int)min(ends[1] - row0, (int64_t)kFewRows), cols = (int)min(a.N - n0, (int64_t)16);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t stride = (uint32_t)a.K * 2;
+    const uint16_t *w = (const uint16_t *)a.b[d] + ((int64_t)j * a.NW + n0) * a.K;
+    const rsrc_t bx = buffer((const uint16_t *)a.a[d] + row0 * a.K, (uint32_t)rows * stride);
+    const rsrc_t bw = buffer(w, (uint32_t)cols * stride), bu = buffer(w + (GLU ? a.N * a.K : 0), (uint32_t)cols * stride);
+    const int K = (int)a.K;
+    const uint32_t line = (uint32_t)(lane & 15) * stride;
+    f32x4 acc[kHalves] = {};
+    constexpr int kFrags = kFewStep / 32, kDeep = 2;
+    for (int k0 = wave * kFewStep; k0 < K; k0 += 4 * kFewStep * kDeep) {
+        typename T::frag x[kDeep][kFrags], g[kDeep][kFrags], u[kDeep][kFrags];
+#pragma unroll
+        for (int s = 0; s < kDeep; s++)
+#pragma unroll
+            for (int i = 0; i < kFrags; i++) {
+                const int k = k0 + s * 4 * kFewStep + i * 32 + (lane >> 4) * 8;
+                const uint32_t at = k < K ? line + k * 2 : kOutside;
+                g[s][i] = load_frag<T>(bw, at);
+                if (GLU) u[s][i] = load_frag<T>(bu, at);
+                x[s][i] = load_frag<T>(bx, at);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < kDeep; s++)
+#pragma unroll
+            for (int i = 0; i < kFrags; i++) {
+                acc[0] = T::mfma(g[s][i], x[s][i], acc[0]);
+                if (GLU) acc[kHalves - 1] = T::mfma(u[s][i], x[s][i], acc[kHalves - 1]);
+            }
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; h++) sums[wave][h][lane] = acc[h];
+    __syncthreads();
+    if (wave != 0) return;
+    f32x4 y[kHalves];
+#pragma unroll
+    for (int h = 0; h < kHalves; h++) {
+        y[h] = sums[0][h][lane];
+#pragma unroll
+        for (int i = 1; i < 4; i++) y[h] += sums[i][h][lane];
+    }
+    // a lane holds columns (lane / 16) * 4 .. + 3 of row lane % 16
+    const int m = lane & 15, c = (lane >> 4) * 4;
+    if (m >= rows || c >= cols) return;
+    const int64_t row = row0 + m, n = n0 + c;
+    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+    u16x4 o;
+#pragma unroll
+    for (int h = 0; h < kHalves; h++) {
+        if (a.has_bias) {
+            const u16x4 b = *(const u16x4 *)((const uint16_t *)a.bias[d] + (int64_t)j * a.NW + h * a.N + n);
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[h][i] += T::to_float(b[i]);
+        }
+        if (a.has_pre) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i] = T::from_float(y[h][i]);
+            *(u16x4 *)((uint16_t *)a.pre[d] + row * a.NW + h * a.N + n) = o;
+        }
+    }
+    u16x4 r = {};
+    if (a.has_residual) r = *(const u16x4 *)((const uint16_t *)a.residual[d] + row * a.N + n);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float v = GLU ? y[0][i] * sigmoid(y[0][i]) * y[kHalves - 1][i] : act_of(a.act, y[0][i]);
+        if (a.has_residual) v += T::to_float(r[i]);
+        o[i] = T::from_float(v);
+    }
+    *(u16x4 *)((uint16_t *)a.out[d] + row * a.N + n) = o;
+}
+
 // ------------------------------------------------------------------ d_pre and the bias
 constexpr int kBlockRows = 64;  // rows of a block of the bias sums
 
@@ -784,9 +883,23 @@ struct DpreArgs {
     int blocks;   // row blocks a tile
 };
 
-// One workgroup per (row block, 256 output columns): a thread walks its
-// column down the block's rows.
-template <typename T>
+// d_pre of one element (and, gated, of its up half) from fp32 values.
+__device__ __forceinline__ void dpre_of(int act, float g, float h, float up, float &dh, float &du) {
+    if (act == A2AV_ACT_SWIGLU) {
+        const float s = sigmoid(h);
+        dh = g * up * (s * (1.0f + h * (1.0f - s)));
+        du = g * h * s;
+    } else {
+        dh = g * act_slope(act, h);
+    }
+}
+
+// One workgroup per (row block, 256 output columns). VEC: a thread has 8
+// neighbouring columns of every eighth row (16-byte loads and stores, four
+// rows in flight), and the eight rows' sums meet in LDS in a fixed order;
+// otherwise a thread walks one column down the block's rows. Bound by the
+// bytes: it reads and writes what it has to once.
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
     if (status_at_entry(a.status)) return;
     const int64_t b = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
@@ -797,35 +910,82 @@ __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
     const int64_t *off = a.offsets + (int64_t)d * (a.P + 1) + j;
     const int64_t r0 = off[0] + ((int64_t)mt * a.blocks + b % a.blocks) * kBlockRows;
     const int64_t r1 = r0 + kBlockRows < off[1] ? r0 + kBlockRows : off[1];
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N || r0 >= r1) return;
-    const bool glu = a.act == A2AV_ACT_SWIGLU;
-    float s0 = 0.0f, s1 = 0.0f;
-    for (int64_t r = r0; r < r1; r++) {
-        const float g = T::to_float(((const uint16_t *)a.d_out[d])[r * a.N + n]);
-        if (a.act == A2AV_ACT_NONE) {
-            s0 += g;
-            continue;
+    if (r0 >= r1) return;  // the same in the whole workgroup
+    const int act = a.act;
+    const bool glu = act == A2AV_ACT_SWIGLU, none = act == A2AV_ACT_NONE;
+    const uint16_t *d_out = (const uint16_t *)a.d_out[d], *pre = (const uint16_t *)a.pre[d];
+    uint16_t *d_pre = (uint16_t *)a.d_pre[d];
+    if constexpr (VEC) {
+        __shared__ float part[2][8][256];
+        const int col = threadIdx.x % 32, group = threadIdx.x / 32;
+        const int64_t n = (int64_t)blockIdx.x * 256 + col * 8;
+        float s0[8] = {}, s1[8] = {};
+        constexpr int kRows = 4;
+        if (n < a.N) {
+            for (int64_t r = r0 + group; r < r1; r += 8 * kRows) {
+                u16x8 g[kRows], h[kRows], up[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; i++) {
+                    const int64_t row = r + i * 8 < r1 ? r + i * 8 : r;  // past the block: row r again, not used
+                    g[i] = *(const u16x8 *)(d_out + row * a.N + n);
+                    if (!none) h[i] = *(const u16x8 *)(pre + row * a.NW + n);
+                    if (glu) up[i] = *(const u16x8 *)(pre + row * a.NW + a.N + n);
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; i++) {
+                    const int64_t row = r + i * 8;
+                    if (row >= r1) break;
+                    float dh[8], du[8];
+#pragma unroll
+                    for (int c = 0; c < 8; c++) {
+                        dh[c] = T::to_float(g[i][c]);
+                        du[c] = 0.0f;
+                        if (!none)
+                            dpre_of(act, dh[c], T::to_float(h[i][c]), glu ? T::to_float(up[i][c]) : 0.0f, dh[c], du[c]);
+                        s0[c] += dh[c];
+                        s1[c] += du[c];
+                    }
+                    if (!none) put8<T>(d_pre + row * a.NW + n, dh);
+                    if (glu) put8<T>(d_pre + row * a.NW + a.N + n, du);
+                }
+            }
         }
-        const uint16_t *pre = (const uint16_t *)a.pre[d] + r * a.NW;
-        uint16_t *d_pre = (uint16_t *)a.d_pre[d] + r * a.NW;
-        const float h = T::to_float(pre[n]);
-        if (glu) {
-            const float up = T::to_float(pre[a.N + n]);
-            const float dg = g * up * act_slope(A2AV_ACT_SILU, h), du = g * h * sigmoid(h);
-            d_pre[n] = T::from_float(dg);
-            d_pre[a.N + n] = T::from_float(du);
-            s0 += dg;
-            s1 += du;
-        } else {
-            const float dh = g * act_slope(a.act, h);
-            d_pre[n] = T::from_float(dh);
+        if (!a.has_bias) return;
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+            part[0][group][col * 8 + c] = s0[c];
+            part[1][group][col * 8 + c] = s1[c];
+        }
+        __syncthreads();
+        const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (m >= a.N) return;
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            x += part[0][i][threadIdx.x];
+            y += part[1][i][threadIdx.x];
+        }
+        a.part[b * a.NW + m] = x;
+        if (glu) a.part[b * a.NW + a.N + m] = y;
+    } else {
+        const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (n >= a.N) return;
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int64_t r = r0; r < r1; r++) {
+            float dh = T::to_float(d_out[r * a.N + n]), du = 0.0f;
+            if (!none) {
+                dpre_of(act, dh, T::to_float(pre[r * a.NW + n]), glu ? T::to_float(pre[r * a.NW + a.N + n]) : 0.0f, dh,
+                        du);
+                d_pre[r * a.NW + n] = T::from_float(dh);
+                if (glu) d_pre[r * a.NW + a.N + n] = T::from_float(du);
+            }
             s0 += dh;
+            s1 += du;
         }
-    }
-    if (a.has_bias) {
-        a.part[b * a.NW + n] = s0;
-        if (glu) a.part[b * a.NW + a.N + n] = s1;
+        if (a.has_bias) {
+            a.part[b * a.NW + n] = s0;
+            if (glu) a.part[b * a.NW + a.N + n] = s1;
+        }
     }
 }
 
@@ -862,8 +1022,8 @@ static int64_t tile_bound(int W, int P, int64_t K, int64_t N, int act, const int
 }
 
 // Tile shapes of the fast products, largest first.
-enum { kBig, kMid, kSmall };
-constexpr int kTile[] = {256, 128, 64};
+enum { kBig, kMid, kSmall, kFew };
+constexpr int kTile[] = {256, 128, 64, kFewRows};
 constexpr int kMostBlocks = 4;  // row blocks of the largest tile
 static_assert(kTile[kBig] == kMostBlocks * kBlockRows && kTile[kSmall] == kBlockRows && kAny == kBlockRows, "");
 
@@ -878,8 +1038,9 @@ struct Layout {
 static bool plan_layout(int W, int P, int64_t K, int64_t N, int act, const int64_t *x_rows, bool with_part,
                         Layout *l) {
     l->tiles = tile_bound(W, P, K, N, act, x_rows, kBlockRows);
-    if (l->tiles < 0) return false;
-    l->first = round256((size_t)(l->tiles + 1) * 8);
+    const int64_t few = tile_bound(W, P, K, N, act, x_rows, kFewRows);
+    if (few < 0) return false;
+    l->first = round256((size_t)(few + 1) * 8);
     l->part = l->first + round256(((size_t)W * P + 1) * 4);
     const int64_t NW = act == A2AV_ACT_SWIGLU ? 2 * N : N;
     const size_t blocks = (size_t)l->tiles + (size_t)(kMostBlocks - 1) * W * P;
@@ -929,6 +1090,15 @@ static void launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, h
         const dim3 g = KIND == kDweight ? dim3(a.cols, a.row_tiles, a.W * a.P) : tile_grid(a.cols, tiles);
         hipLaunchKernelGGL((k_expert_any<KIND, T>), g, dim3(256), 0, stream, a);
         return;
+    }
+    if constexpr (KIND == kForward) {
+        if (shape == kFew) {
+            a.cols = (int)((a.N + 15) / 16);
+            const dim3 g((unsigned)(tiles * a.cols));
+            if (a.act == A2AV_ACT_SWIGLU) hipLaunchKernelGGL((k_expert_few<T, true>), g, dim3(256), 0, stream, a);
+            else hipLaunchKernelGGL((k_expert_few<T, false>), g, dim3(256), 0, stream, a);
+            return;
+        }
     }
     if (KIND == kDweight) tiles = (int64_t)a.W * a.P * a.row_tiles;
     const dim3 g((unsigned)((tiles * a.cols + 7) / 8 * 8));
@@ -1010,7 +1180,12 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     a.has_bias = bias != nullptr;
     a.has_residual = residual != nullptr;
     a.has_pre = pre != nullptr;
-    const int shape = fast ? shape_of(R, (int64_t)W * P, 0, a.NW) : kSmall;
+    const int64_t n = (int64_t)W * P;
+    // Few rows an expert and long weight rows: without LDS. (SwiGLU of 8 rows
+    // on 8 of 32 experts, K 7168, N 2048, bf16: 72 against 107 us; no gate,
+    // 8 experts: 44 against 58 us at K 7168, 55.5 against 55 at K 4096, 58
+    // against 44 at K 2048; 12 rows an expert at K 7168: 210 against 172 us.)
+    const int shape = !fast ? kSmall : R <= 4 * n && K >= 4096 ? kFew : shape_of(R, n, 0, a.NW);
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], (unsigned char *)workspace, l, status, stream);
     launch_product<kForward>(a, type, shape, fast, most_tiles(x_rows, W, P, kTile[shape]), stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
@@ -1057,7 +1232,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
     g.part = (float *)(ws + l.part);
     g.has_bias = d_bias != nullptr;
     int64_t R = 0;
-    bool fast = K % 8 == 0 && N % 8 == 0;
+    bool fast = K % 8 == 0 && N % 8 == 0, vec = N % 8 == 0;
     for (int d = 0; d < W; d++) {
         R += x_rows[d];
         if (!fits(x_rows[d], K) || !fits(x_rows[d], a.NW)) return A2AV_EARG;
@@ -1073,6 +1248,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         a.out[d] = d_x ? d_x[d] : nullptr;
         b.b[d] = x[d];
         b.out[d] = d_weight ? d_weight[d] : nullptr;
+        vec = vec && aligned16(g.pre[d]) && aligned16(d_out[d]) && aligned16(g.d_pre[d]);
         fast = fast && aligned16(a.a[d]) && aligned16(a.b[d]) && aligned16(a.out[d]) && aligned16(b.b[d]) &&
                aligned16(b.out[d]);
     }
@@ -1083,8 +1259,10 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], ws, l, status, stream);
     if (!none || d_bias) {
         const dim3 grid = tile_grid((N + 255) / 256, tiles * g.blocks);
-        if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dpre<Bf16>, grid, dim3(256), 0, stream, g);
-        else hipLaunchKernelGGL(k_expert_dpre<Fp16>, grid, dim3(256), 0, stream, g);
+        if (type == A2AV_DT_BF16 && vec) hipLaunchKernelGGL((k_expert_dpre<Bf16, true>), grid, dim3(256), 0, stream, g);
+        else if (type == A2AV_DT_BF16) hipLaunchKernelGGL((k_expert_dpre<Bf16, false>), grid, dim3(256), 0, stream, g);
+        else if (vec) hipLaunchKernelGGL((k_expert_dpre<Fp16, true>), grid, dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL((k_expert_dpre<Fp16, false>), grid, dim3(256), 0, stream, g);
     }
     if (d_bias) {
         const dim3 grid((unsigned)((a.NW + 255) / 256), W * P);

@@ -225,6 +225,17 @@ def test_large_tiles(shape, kind, act):
     Experts(per, K, N, kind, act, seed + 1).check_backward()
 
 
+@pytest.mark.parametrize("per,K,N", [([[1, 0, 3, 1, 0, 2, 1, 5]], 4104, 72), ([[1]], 7168, 16),
+                                     ([[20, 0, 0, 0, 0, 0, 0, 1], [0, 0, 16, 0, 0, 0, 0, 0]], 4096, 40),
+                                     ([[0, 17, 0, 0, 1, 2, 3, 4]], 5000, 264)], ids=str)
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("act", list(ACTS))
+def test_few_rows_of_long_weights(per, K, N, kind, act):
+    seed = zlib.crc32(repr((per, K, N, kind, act)).encode())
+    Experts(per, K, N, kind, act, seed).check_forward()
+    Experts(per, K, N, kind, act, seed, bias=False, residual=False, pre=False).check_forward()
+
+
 @pytest.mark.parametrize("want", [("d_x",), ("d_weight",), ("d_bias",), ()], ids=str)
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_backward_of_some(want, act):
@@ -242,7 +253,7 @@ def test_residual_in_place():
     Experts([[20, 70]], 64, 48, "bf16", "gelu", 7).check_forward(in_place=True)
 
 
-@pytest.mark.parametrize("K,N", [(64, 64), (72, 40), (33, 31), (1024, 512)])
+@pytest.mark.parametrize("K,N", [(64, 64), (72, 40), (33, 31), (1024, 512), (4096, 24)])
 def test_other_experts_infinities_stay_out(K, N):
     """An expert whose rows and weights are infinite or NaN leaves its
     neighbours' results as they are."""

@@ -1,6 +1,7 @@
 // route.hip — the router in front of the MoE pack, and its gradient (gfx950).
 //
-//   k_moe_route           expert ids and gate weights of every token
+//   k_moe_route           expert ids and gate weights, 16 or 64 lanes a token
+//   k_moe_route_exact     the same by one wave a token, for any size
 //   k_route_check         range check of the ids the gradient scatters to
 //   k_moe_route_backward  the gradient of the weights in the logits
 #include <hip/hip_runtime.h>
@@ -10,6 +11,8 @@
 #include "common.hpp"
 
 namespace a2av {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxGroups = 64;
 
@@ -50,43 +53,36 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// One token by one wave, every comparison in double as the result is defined:
-// scores and keys of all experts into LDS, the groups' scores by one lane
-// each, then k rounds of a wave-wide argmax. Lane j ends with id j and its
-// score in *id and *p; the return value tells a token that has NaN weights.
+// One token's ids by one wave, every comparison in double as the result is
+// defined: scores and keys of all experts into LDS, the groups' scores by one
+// lane each, then k rounds of a wave-wide argmax. Lane j returns id j; *bad
+// tells a token that has NaN weights.
 template <int TYPE>
-__device__ __forceinline__ bool route_exact(const RouteArgs &a, const void *row, double *key,
-                                            int lane, int *id, double *p) {
+__device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, double *key, int lane, bool *bad) {
     const double inf = __builtin_huge_val(), nan = __builtin_nan("");
     const int E = a.E;
     double m = -inf;
-    int bad = 0;
+    int off = 0;
     for (int e = lane; e < E; e += kWave) {
         const double z = logit_at<TYPE>(row, e);
-        bad |= z != z || (!a.sigmoid && z == inf);
+        off |= z != z || (!a.sigmoid && z == inf);
         m = fmax(m, z);
     }
-    *id = lane;
-    *p = nan;
-    if (__ballot(bad)) return true;
-    double inv = 1.0;
+    *bad = __ballot(off) != 0;
+    if (*bad) return lane;
+    double sum = 0;
     if (!a.sigmoid) {
         m = wave_max(m);
-        double sum = 0;
         for (int e = lane; e < E; e += kWave) {
             const double z = logit_at<TYPE>(row, e);
             if (z != -inf) sum += exp(z - m);
         }
         sum = wave_sum(sum);
-        inv = sum;
     }
-    const auto score = [&](double z) {
-        if (z == -inf) return 0.0;
-        return a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / inv;
-    };
     for (int e = lane; e < E; e += kWave) {
         const double z = logit_at<TYPE>(row, e);
-        double c = score(z) + (a.bias ? (double)a.bias[e] : 0.0);
+        double c = a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / sum;
+        if (a.bias) c += a.bias[e];
         if (z == -inf || c != c) c = -inf;
         key[e] = c;
     }
@@ -120,6 +116,7 @@ __device__ __forceinline__ bool route_exact(const RouteArgs &a, const void *row,
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    int id = 0;
     for (int j = 0; j < a.k; j++) {
         double c = -inf;
         float z = -__builtin_huge_valf();
@@ -144,21 +141,106 @@ __device__ __forceinline__ bool route_exact(const RouteArgs &a, const void *row,
             z = take ? oz : z;
             best = take ? oe : best;
         }
-        if (lane == j) {
-            *id = best;
-            *p = score(z);
-        }
+        if (lane == j) id = best;
         if (lane == 0) key[best] = nan;
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    return false;
+    return id;
 }
 
-// One wave per token.
+// Reductions over the L lanes of a token (16: a DPP row), in an order that is
+// the same for all of them.
+template <int L, typename F>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t x, F op) {
+    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, false));  // row_ror:8
+    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xf, 0xf, false));
+    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xf, 0xf, false));
+    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xf, 0xf, false));
+    if constexpr (L == 64) {
+        x = op(x, (uint32_t)__shfl_xor((int)x, 16));
+        x = op(x, (uint32_t)__shfl_xor((int)x, 32));
+    }
+    return x;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max_u32(uint32_t v) {
+    return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// The weights of the ids that lanes 0 .. k - 1 of a token (and those after
+// them, L apart) hold in sel: fp32, from the chosen logits relative to the
+// largest of them, so that scores outside fp32's range still have ratios; what
+// is 0 in double (e^-709 and less) is 0 here. m: the largest of all logits,
+// for softmax; sum: the softmax's, without renorm.
+template <int TYPE, int L>
+__device__ __forceinline__ void route_weights(const RouteArgs &a, const void *row, const int *sel, int sub, bool bad,
+                                              float m, float sum, int32_t *ids, float *w, bool store) {
+    const float inf = __builtin_huge_valf();
+    float top = -inf;
+    for (int j = sub; j < a.k; j += L) top = fmaxf(top, logit_at<TYPE>(row, sel[j]));
+    top = lanes_max<L>(top);
+    const float least = a.sigmoid ? -709.0f : m - 745.0f;
+    const bool nothing = !(top >= least) || top == -inf;
+    const float ref = a.sigmoid ? fminf(top, 0.0f) : a.renorm ? top : m;
+    const auto score = [&](float z) {
+        if (z == -inf || z < least) return 0.0f;
+        if (!a.sigmoid) return expf(z - ref);
+        if (z >= 0.0f) return 1.0f / (1.0f + expf(-z));
+        return expf(a.renorm ? z - ref : z) / (1.0f + expf(z));
+    };
+    float S = 0.0f;
+    if (a.renorm) {
+        for (int j = sub; j < a.k; j += L) S += score(logit_at<TYPE>(row, sel[j]));
+        S = lanes_sum<L>(S);
+    } else {
+        S = a.sigmoid ? 1.0f : sum;
+    }
+    for (int j = sub; j < a.k; j += L) {
+        const int id = sel[j];
+        float v = nothing ? 0.0f : score(logit_at<TYPE>(row, id)) / S * a.scale;
+        if (bad) v = __builtin_nanf("");
+        if (store) {
+            ids[j] = id;
+            w[j] = v;
+        }
+    }
+}
+
+// m and sum of a whole row by one wave, as route_weights wants them.
 template <int TYPE>
-__global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a) {
+__device__ __forceinline__ void row_sum(const RouteArgs &a, const void *row, int lane, float *m, float *sum) {
+    *m = *sum = 0.0f;
+    if (a.sigmoid) return;
+    float x = -__builtin_huge_valf(), s = 0.0f;
+    for (int e = lane; e < a.E; e += kWave) x = fmaxf(x, logit_at<TYPE>(row, e));
+    x = lanes_max<kWave>(x);
+    *m = x;
+    if (a.renorm) return;
+    for (int e = lane; e < a.E; e += kWave) {
+        const float z = logit_at<TYPE>(row, e);
+        s += z == -__builtin_huge_valf() ? 0.0f : expf(z - x);
+    }
+    *sum = lanes_sum<kWave>(s);
+}
+
+// One wave per token: any size.
+template <int TYPE>
+__global__ __launch_bounds__(256) void k_moe_route_exact(const RouteArgs a) {
     extern __shared__ double keys[];
+    __shared__ int sel[4][kWave];
     if (status_at_entry(a.status)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int waves = blockDim.x / kWave;
@@ -167,17 +249,238 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a) {
     for (int64_t i = (int64_t)blockIdx.x * waves + wave; i < n; i += (int64_t)gridDim.x * waves) {
         const int r = (int)(i / a.T);
         const int64_t t = i - (int64_t)r * a.T;
-        int id;
-        double p;
-        route_exact<TYPE>(a, logit_row<TYPE>(a.z[r], t, a.E), key, lane, &id, &p);
-        if (a.renorm) {
-            const double S = wave_sum(lane < a.k ? p : 0.0);
-            p = S == 0 ? 0.0 : p / S;
+        const void *row = logit_row<TYPE>(a.z[r], t, a.E);
+        bool bad;
+        float m, sum;
+        sel[wave][lane] = route_exact<TYPE>(a, row, key, lane, &bad);
+        row_sum<TYPE>(a, row, lane, &m, &sum);
+        route_weights<TYPE, kWave>(a, row, sel[wave], lane, bad, m, sum, a.ids[r] + t * a.k, a.w[r] + t * a.k, true);
+    }
+}
+
+// Doubles of LDS a wave needs.
+__host__ __device__ inline int route_keys(int E, int tokens, int groups) {
+    return groups > 1 && tokens > 2 ? (E * tokens + 1) / 2 : E;
+}
+
+// L lanes per token, V logits per lane (blocks of 4 neighbours, L blocks
+// apart), so E <= L * V. Each lane sorts its keys, and the rounds of the
+// selection compare the lanes' heads: 4 DPP steps a round for the four tokens
+// of a wave at 16 lanes each. The keys are compared as 32-bit integers whose
+// low bits hold the place:
+//   BY_LOGIT (no bias, no group sums: the keys' order is the logits')  16-bit
+//     logits leave 13 bits for the whole id, and ties are decided; fp32
+//     logits lose 4 bits to the place in the lane
+//   else  keys in fp32, whose distance from the exact ones is bounded
+// A token in which two neighbours of the k + 1 best (or the groups at the
+// border) are nearer than what was lost is done again by route_exact: the
+// result is always the defined one. Moves E logits per token; bound by the
+// VALU work of the sort and the rounds.
+template <int TYPE, int L, int V, bool BY_LOGIT>
+__global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) {
+    constexpr bool kIds = BY_LOGIT && TYPE != A2AV_DT_F32;   // whole ids in the keys
+    constexpr uint32_t kLow = kIds ? 0x1fff : V - 1;
+    constexpr int kTokens = kWave / L, kWaves = 4;
+    extern __shared__ double keys[];  // a wave's exact keys of one token, or its tokens' fp32 keys
+    __shared__ uint32_t sorted[kWaves][V][kWave];
+    __shared__ int sel[kWaves][kTokens][kWave];
+    if (status_at_entry(a.status)) return;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int sub = lane & (L - 1), mine = lane / L;
+    const int E = a.E, k = a.k;
+    const float inf = __builtin_huge_valf();
+    double *key = keys + (size_t)wave * route_keys(E, kTokens, a.groups);
+    float *group_keys = (float *)key + mine * E;
+    const int64_t n = (int64_t)a.W * a.T;
+    const bool full = !a.sigmoid && (!BY_LOGIT || !a.renorm);  // needs the softmax's sum
+    const uint64_t my_lanes = L == 64 ? ~0ull : 0xffffull << (lane & 48);
+    for (int64_t i0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens; i0 < n; i0 += (int64_t)gridDim.x * kWaves * kTokens) {
+        const bool store = i0 + mine < n;
+        const int64_t i = store ? i0 + mine : n - 1;
+        const int r = (int)(i / a.T);
+        const int64_t t = i - (int64_t)r * a.T;
+        const void *row = logit_row<TYPE>(a.z[r], t, E);
+        float z[V];
+        int bad = 0;
+        if (vec) {
+#pragma unroll
+            for (int c = 0; c < V / 4; c++) {
+                const int e = (c * L + sub) * 4;
+                if constexpr (TYPE == A2AV_DT_F32) {
+                    f32x4 v = {-inf, -inf, -inf, -inf};
+                    if (e < E) v = *(const f32x4 *)((const float *)row + e);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) z[c * 4 + q] = v[q];
+                } else {
+                    u32x2 v = {0, 0};
+                    if (e < E) v = *(const u32x2 *)((const uint16_t *)row + e);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const uint16_t h = (uint16_t)(v[q / 2] >> (q % 2 * 16));
+                        z[c * 4 + q] = e < E ? logit_at<TYPE>(&h, 0) : -inf;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const int e = ((v / 4) * L + sub) * 4 + v % 4;
+                z[v] = e < E ? logit_at<TYPE>(row, e) : -inf;
+            }
         }
-        if (lane < a.k) {
-            a.ids[r][t * a.k + lane] = id;
-            a.w[r][t * a.k + lane] = (float)(p * a.scale);
+        float m = -inf;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            bad |= z[v] != z[v] || (!a.sigmoid && z[v] == inf);
+            m = fmaxf(m, z[v]);
         }
+        const bool is_bad = (__ballot(bad) & my_lanes) != 0;
+        float sum = 0.0f, key_err = 0.0f;
+        float c[V];
+        m = lanes_max<L>(m);
+        if (full) {
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                c[v] = z[v] == -inf ? 0.0f : __expf(z[v] - m);
+                sum += c[v];
+            }
+            sum = lanes_sum<L>(sum);
+        }
+        if constexpr (BY_LOGIT) {
+#pragma unroll
+            for (int v = 0; v < V; v++) c[v] = z[v];
+        } else {
+            // sigmoid: the exponential's relative error is |z| 2^-23 at most and
+            // s (1 - s) |z| < 0.23, with a step each of the sum and the
+            // reciprocal under 2^-21 in all; softmax: a step for every term of
+            // the sum and a few more, relative to at most 1 / sum
+            key_err = a.sigmoid ? 0x1p-20f : (V + 40) * 0x1p-23f / sum;
+            const float scale = a.sigmoid ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const int e = ((v / 4) * L + sub) * 4 + v % 4;
+                float s = a.sigmoid ? 1.0f / (1.0f + __expf(-z[v])) : c[v] * scale;
+                if (a.bias && e < E) s += a.bias[e];
+                c[v] = z[v] == -inf || s != s ? -inf : s;
+            }
+        }
+        bool unsure = false;
+        uint32_t kept = ~0u;
+        if (a.groups > 1) {
+            const int per = E / a.groups;
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const int e = ((v / 4) * L + sub) * 4 + v % 4;
+                if (e < E) group_keys[e] = c[v];
+            }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            float t1 = -inf, t2 = -inf;
+            if (sub < a.groups) {
+                int at = sub % per;  // the lanes start at different banks
+                for (int q = 0; q < per; q++) {
+                    const float x = group_keys[sub * per + at];
+                    t2 = fmaxf(t2, fminf(t1, x));
+                    t1 = fmaxf(t1, x);
+                    at = at + 1 == per ? 0 : at + 1;
+                }
+            }
+            float gs = a.group_top == 1 ? t1 : t1 + t2;
+            if (gs != gs) gs = -inf;
+            int before = 0;
+            for (int g = 0; g < a.groups; g++) {
+                const float o = __shfl(gs, g, L);
+                before += o > gs || (o == gs && g < sub);
+            }
+            const bool in = sub < a.groups && before < a.topk_groups;
+            kept = (uint32_t)((__ballot(in) >> (L == 64 ? 0 : lane & 48)));
+            if constexpr (!BY_LOGIT) {
+                const float low = -lanes_max<L>(in ? -gs : -inf), high = lanes_max<L>(sub < a.groups && !in ? gs : -inf);
+                unsure = !(low - high > 4 * key_err + 0x1p-20f * fmaxf(fabsf(low), fabsf(high)));
+                if (high == -inf && low > -inf) unsure = false;
+            }
+        }
+        uint32_t s[V];
+        const float per_group = a.groups > 1 ? 1.0f / (float)(E / a.groups) : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int e = ((v / 4) * L + sub) * 4 + v % 4;
+            const uint32_t u = __float_as_uint(c[v] + 0.0f);  // -0 counts as 0
+            const uint32_t o = u ^ ((int)u < 0 ? 0xffffffffu : 0x80000000u);
+            s[v] = (o & ~kLow) | (kIds ? kLow - e : kLow - v);
+            bool live = e < E;
+            if (a.groups > 1) live = live && ((kept >> (int)(((float)e + 0.5f) * per_group)) & 1);
+            s[v] = live ? s[v] : 0;
+        }
+        // Batcher's odd-even merge sort, descending
+#pragma unroll
+        for (int p = 1; p < V; p *= 2)
+#pragma unroll
+            for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+                for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                    for (int x = 0; x < q; x++)
+                        if (x + j + q < V && (x + j) / (2 * p) == (x + j + q) / (2 * p)) {
+                            const uint32_t hi = max(s[x + j], s[x + j + q]), lo = min(s[x + j], s[x + j + q]);
+                            s[x + j] = hi;
+                            s[x + j + q] = lo;
+                        }
+#pragma unroll
+        for (int v = 0; v < V; v++) sorted[wave][v][lane] = s[v];
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        uint32_t head = s[0], last = 0;
+        int at = 0;
+        const int rounds = k < E ? k + 1 : k;  // one more: the border
+        for (int j = 0; j < rounds; j++) {
+            const uint32_t top = lanes_max_u32<L>(head);
+            if constexpr (!kIds) {
+                if (j > 0) {
+                    if constexpr (BY_LOGIT) {
+                        unsure |= (top & ~kLow) == (last & ~kLow);
+                    } else if (top != 0) {  // 0: no expert is left
+                        const uint32_t x = last & ~kLow, y = top & ~kLow;
+                        const float hi = __uint_as_float(x ^ ((int)x < 0 ? 0x80000000u : 0xffffffffu));
+                        const float lo = __uint_as_float(y ^ ((int)y < 0 ? 0x80000000u : 0xffffffffu));
+                        unsure |= !(hi - lo > 2 * key_err + 0x1p-18f * fmaxf(fabsf(hi), fabsf(lo)));
+                    }
+                }
+                last = top;
+            }
+            const bool win = head == top;
+            if constexpr (!kIds) {  // the same key in two lanes
+                const uint64_t won = __ballot(win) & my_lanes;
+                unsure |= top != 0 && (won & (won - 1)) != 0;
+            }
+            if (win && j < k) {
+                const int v = (int)(kLow - (top & kLow));
+                sel[wave][mine][j] = kIds ? v : ((v / 4) * L + sub) * 4 + v % 4;
+            }
+            at += win;
+            if (win) head = at < V ? sorted[wave][at][lane] : 0;
+        }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (is_bad || !store) {
+            for (int j = sub; j < k; j += L) sel[wave][mine][j] = j;
+            unsure = false;
+        }
+        // tokens to do again, one after the other, by the whole wave
+        uint64_t again = __ballot(unsure && sub == 0);
+        while (again) {
+            const int l = __builtin_ctzll(again);
+            again &= again - 1;
+            const int64_t i2 = i0 + l / L;
+            const int r2 = (int)(i2 / a.T);
+            const void *row2 = logit_row<TYPE>(a.z[r2], i2 - (int64_t)r2 * a.T, E);
+            bool none;
+            const int id = route_exact<TYPE>(a, row2, key, lane, &none);
+            if (lane < k) sel[wave][l / L][lane] = id;
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        route_weights<TYPE, L>(a, row, sel[wave][mine], sub, is_bad, m, sum, a.ids[r] + t * k, a.w[r] + t * k, store);
     }
 }
 
@@ -287,6 +590,34 @@ static unsigned wave_grid(int64_t waves, int per_block) {
     return (unsigned)blocks;
 }
 
+template <int TYPE, int L, int V>
+static void launch_route(const RouteArgs &a, bool by_logit, bool vec, hipStream_t stream) {
+    const unsigned blocks = wave_grid(((int64_t)a.W * a.T * L + kWave - 1) / kWave, 4);
+    const unsigned lds = (unsigned)(4 * route_keys(a.E, kWave / L, a.groups) * sizeof(double));
+    if (by_logit) hipLaunchKernelGGL((k_moe_route<TYPE, L, V, true>), dim3(blocks), dim3(256), lds, stream, a, vec);
+    else hipLaunchKernelGGL((k_moe_route<TYPE, L, V, false>), dim3(blocks), dim3(256), lds, stream, a, vec);
+}
+
+template <int TYPE>
+static void launch_route(const RouteArgs &a, bool vec, hipStream_t stream) {
+    // the order of the keys is that of the logits: no bias, and no sums of scores
+    const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+    const int E = a.E;
+    if (E > 1024 || (a.groups > 1 && a.groups > (E <= 256 ? 16 : 32))) {
+        const int waves = E <= 1024 ? 4 : 1;
+        hipLaunchKernelGGL(k_moe_route_exact<TYPE>, dim3(wave_grid((int64_t)a.W * a.T, waves)), dim3(waves * kWave),
+                           (unsigned)(waves * E * sizeof(double)), stream, a);
+    } else if (E <= 64) {
+        launch_route<TYPE, 16, 4>(a, by_logit, vec, stream);
+    } else if (E <= 128) {
+        launch_route<TYPE, 16, 8>(a, by_logit, vec, stream);
+    } else if (E <= 256) {
+        launch_route<TYPE, 16, 16>(a, by_logit, vec, stream);
+    } else {
+        launch_route<TYPE, 64, 16>(a, by_logit, vec, stream);
+    }
+}
+
 }  // namespace a2av
 
 using namespace a2av;
@@ -322,12 +653,12 @@ A2AV_API int moe_route(int W, int64_t T, int k, int E, int type, int score,
     a.renorm = renorm != 0;
     a.scale = scale;
     if (T == 0) return A2AV_OK;
-    const int waves = E <= 1024 ? 4 : 1;
-    const unsigned blocks = wave_grid((int64_t)W * T, waves), lds = (unsigned)(waves * E * sizeof(double));
+    bool vec = E % 4 == 0;
+    for (int r = 0; r < W; r++) vec = vec && (uintptr_t)logits[r] % 16 == 0;
     switch (type) {
-    case A2AV_DT_F32: hipLaunchKernelGGL(k_moe_route<A2AV_DT_F32>, dim3(blocks), dim3(waves * kWave), lds, stream, a); break;
-    case A2AV_DT_BF16: hipLaunchKernelGGL(k_moe_route<A2AV_DT_BF16>, dim3(blocks), dim3(waves * kWave), lds, stream, a); break;
-    default: hipLaunchKernelGGL(k_moe_route<A2AV_DT_F16>, dim3(blocks), dim3(waves * kWave), lds, stream, a); break;
+    case A2AV_DT_F32: launch_route<A2AV_DT_F32>(a, vec, stream); break;
+    case A2AV_DT_BF16: launch_route<A2AV_DT_BF16>(a, vec, stream); break;
+    default: launch_route<A2AV_DT_F16>(a, vec, stream); break;
     }
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

@@ -520,6 +520,7 @@ int moe_combine_grouped(int W, int64_t T, int k, int E, int64_t H, const int64_t
  * lowest id. The bias (of a load balancer) only selects:
  *   weights[j] = scale * s[id_j]                          (renorm 0)
  *   weights[j] = scale * s[id_j] / sum_i s[id_i], or 0 if that sum is 0  (1)
+ * (in fp32; a score that double rounds to 0, at about e^-709, is 0)
  *   k, E           1 <= k <= min(64, topk_groups * E / groups),
  *                  E <= A2AV_MAX_EXPERTS (E % W is not asked for here)
  *   groups         divides E, at most 64; 1 <= topk_groups <= groups;

@@ -194,6 +194,9 @@ def _i64_array(vals):
     return arr
 
 
+_PTRS = [ctypes.c_void_p * n for n in range(MAX_W + 1)]
+
+
 def _typed(tensors, name, dtype, sizes):
     """Pointers of one array per rank (None: no arrays), each on the GPU,
     contiguous, of this type and with at least this many elements."""
@@ -201,14 +204,17 @@ def _typed(tensors, name, dtype, sizes):
         return None
     if len(tensors) != len(sizes):
         raise ValueError(f"{name} needs {len(sizes)} entries")
-    arr = (ctypes.c_void_p * len(sizes))()
-    for i, (t, n) in enumerate(zip(tensors, sizes)):
-        if t is None:
-            if n > 0:
+    ptrs = []
+    for t, n in zip(tensors, sizes):
+        # the usual case without a call per check; anything else is looked into
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
+            ptrs.append(t.data_ptr())
+        else:
+            i = len(ptrs)
+            if t is None and n > 0:
                 raise ValueError(f"{name}[{i}] needs {n} elements")
-            continue
-        arr[i] = _one(t, f"{name}[{i}]", dtype, n)
-    return arr
+            ptrs.append(None if t is None else _one(t, f"{name}[{i}]", dtype, n))
+    return _PTRS[len(ptrs)](*ptrs) if len(ptrs) <= MAX_W else (ctypes.c_void_p * len(ptrs))(*ptrs)
 
 
 def _one(t, name, dtype, n):
@@ -225,15 +231,19 @@ def _check(fn, rc):
         raise A2avError(fn, rc)
 
 
-def _call(fn, like, *args):
-    """The C entry point with the tensors' GPU current: the kernels of a stream
-    are launched on the GPU that is current."""
-    f = getattr(lib(), fn)
-    if like.device.index == torch.cuda.current_device():
-        _check(fn, f(*args))
-        return
-    with torch.cuda.device(like.device):
-        _check(fn, f(*args))
+def _call(fn, like, stream, *args):
+    """The C entry point on `stream` (or the current one of `like`'s GPU), with
+    that GPU current: the kernels of a stream are launched on the GPU that is
+    current."""
+    f = getattr(_lib or lib(), fn)
+    device = like.device.index
+    if device == torch.cuda.current_device():
+        rc = f(*args, _stream(stream, like))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, _stream(stream, like))
+    if rc != OK:
+        raise A2avError(fn, rc)
 
 
 # ------------------------------------------------------------------ entry points
@@ -453,26 +463,24 @@ def moe_route(W, T, k, E, score, logits, bias, groups, topk_groups, group_top, r
     bias (fp32 [E] or None), the best topk_groups of groups, the k best
     experts, renormalised and scaled."""
     dtype = _logits_type(logits)
-    _call("moe_route", status, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
+    _call("moe_route", status, stream, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
           _typed(logits, "logits", dtype, [T * E] * W),
           None if bias is None else _one(bias, "bias", torch.float32, E), int(groups),
           int(topk_groups), int(group_top), int(bool(renorm)), float(scale),
           _typed(ids, "ids", torch.int32, [T * k] * W),
-          _typed(weights, "weights", torch.float32, [T * k] * W), _dev(status, "status"),
-          _stream(stream, status))
+          _typed(weights, "weights", torch.float32, [T * k] * W), _dev(status, "status"))
 
 
 def moe_route_backward(W, T, k, E, score, logits, ids, weights, renorm, scale, d_weights, d_logits,
                        status, stream=None):
     """The gradient of moe_route's weights in its logits, the ids held fixed."""
     dtype = _logits_type(logits)
-    _call("moe_route_backward", status, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
+    _call("moe_route_backward", status, stream, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
           _typed(logits, "logits", dtype, [T * E] * W),
           _typed(ids, "ids", torch.int32, [T * k] * W),
           _typed(weights, "weights", torch.float32, [T * k] * W), int(bool(renorm)), float(scale),
           _typed(d_weights, "d_weights", torch.float32, [T * k] * W),
-          _typed(d_logits, "d_logits", dtype, [T * E] * W), _dev(status, "status"),
-          _stream(stream, status))
+          _typed(d_logits, "d_logits", dtype, [T * E] * W), _dev(status, "status"))
 
 
 def _logits_type(logits):
@@ -490,13 +498,13 @@ def moe_combine_backward(W, T, k, H, back, perm, weights, d_out, d_back, d_weigh
     """The gradient of moe_combine in its rows (d_back, bf16) and its weights
     (d_weights, fp32), from d_out (bf16 [T, H] per rank)."""
     bf16, rows, toks = torch.bfloat16, [T * k * H] * W, [T * H] * W
-    _call("moe_combine_backward", status, int(W), int(T), int(k), int(H),
+    _call("moe_combine_backward", status, stream, int(W), int(T), int(k), int(H),
           _typed(back, "back", bf16, rows), _typed(perm, "perm", torch.int64, [T * k] * W),
           _typed(weights, "weights", torch.float32, [T * k] * W),
           _typed(d_out, "d_out", bf16, toks), _typed(d_back, "d_back", bf16, rows),
           _typed(d_weights, "d_weights", torch.float32, [T * k] * W),
           _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-          _dev(status, "status"), _stream(stream, status))
+          _dev(status, "status"))
 
 
 def moe_combine_return_backward_workspace_bytes(W, T, k, E) -> int:
@@ -510,7 +518,7 @@ def moe_combine_return_backward(W, T, k, E, H, expert_counts, ids, perm, recv, r
     bf16, rows = torch.bfloat16, [int(n) * H for n in recv_rows]
     if len(rows) != W:
         raise ValueError("recv_rows needs W entries")
-    _call("moe_combine_return_backward", status, int(W), int(T), int(k), int(E), int(H),
+    _call("moe_combine_return_backward", status, stream, int(W), int(T), int(k), int(E), int(H),
           _one(expert_counts, "expert_counts", torch.int64, W * E),
           _typed(ids, "ids", torch.int32, [T * k] * W),
           _typed(perm, "perm", torch.int64, [T * k] * W), _typed(recv, "recv", bf16, rows),
@@ -518,7 +526,7 @@ def moe_combine_return_backward(W, T, k, E, H, expert_counts, ids, perm, recv, r
           _typed(d_out, "d_out", bf16, [T * H] * W), _typed(d_recv, "d_recv", bf16, rows),
           _typed(d_weights, "d_weights", torch.float32, [T * k] * W), int(layout),
           _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-          _dev(status, "status"), _stream(stream, status))
+          _dev(status, "status"))
 
 
 def _expert_type(x):
@@ -545,14 +553,14 @@ def moe_expert_linear(W, P, K, N, act, x, x_rows, expert_offsets, weight, bias, 
     if len(x_rows) != W:
         raise ValueError("x_rows needs W entries")
     narrow, wide = [int(n) * N for n in x_rows], [int(n) * NW for n in x_rows]
-    _call("moe_expert_linear", status, int(W), int(P), int(K), int(N), _TYPES[dtype], int(act),
+    _call("moe_expert_linear", status, stream, int(W), int(P), int(K), int(N), _TYPES[dtype], int(act),
           _typed(x, "x", dtype, [int(n) * K for n in x_rows]), _i64_array(x_rows),
           _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
           _typed(weight, "weight", dtype, [P * NW * K] * W),
           _typed(bias, "bias", dtype, [P * NW] * W), _typed(residual, "residual", dtype, narrow),
           _typed(out, "out", dtype, narrow), _typed(pre, "pre", dtype, wide),
           _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-          _dev(status, "status"), _stream(stream, status))
+          _dev(status, "status"))
 
 
 def moe_expert_linear_backward_workspace_bytes(W, P, K, N, act, x_rows) -> int:
@@ -570,7 +578,7 @@ def moe_expert_linear_backward(W, P, K, N, act, x, x_rows, expert_offsets, weigh
     if len(x_rows) != W:
         raise ValueError("x_rows needs W entries")
     wide, xs, ws = [int(n) * NW for n in x_rows], [int(n) * K for n in x_rows], [P * NW * K] * W
-    _call("moe_expert_linear_backward", status, int(W), int(P), int(K), int(N), _TYPES[dtype],
+    _call("moe_expert_linear_backward", status, stream, int(W), int(P), int(K), int(N), _TYPES[dtype],
           int(act), _typed(x, "x", dtype, xs), _i64_array(x_rows),
           _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
           _typed(weight, "weight", dtype, ws), _typed(pre, "pre", dtype, wide),
@@ -578,7 +586,7 @@ def moe_expert_linear_backward(W, P, K, N, act, x, x_rows, expert_offsets, weigh
           _typed(d_pre, "d_pre", dtype, wide), _typed(d_x, "d_x", dtype, xs),
           _typed(d_weight, "d_weight", dtype, ws), _typed(d_bias, "d_bias", dtype, [P * NW] * W),
           _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-          _dev(status, "status"), _stream(stream, status))
+          _dev(status, "status"))
 
 
 def keys_bucketize_workspace_bytes(W, n_tables) -> int:

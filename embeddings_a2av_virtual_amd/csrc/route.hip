@@ -3,7 +3,9 @@
 //   k_moe_route           expert ids and gate weights, 16 or 64 lanes a token
 //   k_moe_route_exact     the same by one wave a token, for any size
 //   k_route_check         range check of the ids the gradient scatters to
-//   k_moe_route_backward  the gradient of the weights in the logits
+//   k_moe_route_backward  the gradient of the weights in the logits, 16 or 64
+//                         lanes a token
+//   k_moe_route_backward_any  the same by one wave a token, for any size
 #include <hip/hip_runtime.h>
 
 #include <cstring>
@@ -63,6 +65,7 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
     const int E = a.E;
     double m = -inf;
     int off = 0;
+#pragma unroll 1
     for (int e = lane; e < E; e += kWave) {
         const double z = logit_at<TYPE>(row, e);
         off |= z != z || (!a.sigmoid && z == inf);
@@ -73,12 +76,14 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
     double sum = 0;
     if (!a.sigmoid) {
         m = wave_max(m);
+#pragma unroll 1
         for (int e = lane; e < E; e += kWave) {
             const double z = logit_at<TYPE>(row, e);
             if (z != -inf) sum += exp(z - m);
         }
         sum = wave_sum(sum);
     }
+#pragma unroll 1
     for (int e = lane; e < E; e += kWave) {
         const double z = logit_at<TYPE>(row, e);
         double c = a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / sum;
@@ -93,6 +98,7 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
         double gs = -inf;
         if (lane < a.groups) {
             double t1 = -inf, t2 = -inf;
+#pragma unroll 1
             for (int i = 0; i < per; i++) {
                 const double c = key[lane * per + i];
                 if (c > t1) {
@@ -106,21 +112,25 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
             if (gs != gs) gs = -inf;
         }
         int before = 0;
+#pragma unroll 1
         for (int g = 0; g < a.groups; g++) {
             const double o = __shfl(gs, g);
             before += o > gs || (o == gs && g < lane);
         }
         const uint64_t kept = __ballot(lane < a.groups && before < a.topk_groups);
+#pragma unroll 1
         for (int e = lane; e < E; e += kWave)
             if (!((kept >> (e / per)) & 1)) key[e] = nan;
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     int id = 0;
+#pragma unroll 1
     for (int j = 0; j < a.k; j++) {
         double c = -inf;
         float z = -__builtin_huge_valf();
         int best = E;  // no expert: behind every real one
+#pragma unroll 1
         for (int e = lane; e < E; e += kWave) {
             const double o = key[e];
             if (o != o) continue;  // taken, or of a dropped group
@@ -131,7 +141,7 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
                 best = e;
             }
         }
-#pragma unroll
+#pragma unroll 1
         for (int o = 32; o; o >>= 1) {
             const double oc = __shfl_xor(c, o);
             const float oz = __shfl_xor(z, o);
@@ -153,10 +163,10 @@ __device__ __forceinline__ int route_exact(const RouteArgs &a, const void *row, 
 // the same for all of them.
 template <int L, typename F>
 __device__ __forceinline__ uint32_t lanes_reduce(uint32_t x, F op) {
-    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, false));  // row_ror:8
-    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xf, 0xf, false));
-    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xf, 0xf, false));
-    x = op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xf, 0xf, false));
+    x = op(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xf, 0xf, true));  // row_ror:8
+    x = op(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x124, 0xf, 0xf, true));
+    x = op(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x122, 0xf, 0xf, true));
+    x = op(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x121, 0xf, 0xf, true));
     if constexpr (L == 64) {
         x = op(x, (uint32_t)__shfl_xor((int)x, 16));
         x = op(x, (uint32_t)__shfl_xor((int)x, 32));
@@ -180,6 +190,39 @@ __device__ __forceinline__ uint32_t lanes_max_u32(uint32_t v) {
     return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
+// A token's logits over its L lanes: lane sub has 4 neighbours of every 4 * L,
+// -inf past the last.
+template <int TYPE, int L, int V>
+__device__ __forceinline__ void load_logits(const void *row, int E, int sub, bool vec, float (&z)[V]) {
+    const float inf = __builtin_huge_valf();
+    if (vec) {
+#pragma unroll
+        for (int c = 0; c < V / 4; c++) {
+            const int e = (c * L + sub) * 4;
+            if constexpr (TYPE == A2AV_DT_F32) {
+                f32x4 v = {-inf, -inf, -inf, -inf};
+                if (e < E) v = *(const f32x4 *)((const float *)row + e);
+#pragma unroll
+                for (int q = 0; q < 4; q++) z[c * 4 + q] = v[q];
+            } else {
+                u32x2 v = {0, 0};
+                if (e < E) v = *(const u32x2 *)((const uint16_t *)row + e);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const uint16_t h = (uint16_t)(v[q / 2] >> (q % 2 * 16));
+                    z[c * 4 + q] = e < E ? logit_at<TYPE>(&h, 0) : -inf;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int e = ((v / 4) * L + sub) * 4 + v % 4;
+            z[v] = e < E ? logit_at<TYPE>(row, e) : -inf;
+        }
+    }
+}
+
 // The weights of the ids that lanes 0 .. k - 1 of a token (and those after
 // them, L apart) hold in sel: fp32, from the chosen logits relative to the
 // largest of them, so that scores outside fp32's range still have ratios; what
@@ -189,8 +232,11 @@ template <int TYPE, int L>
 __device__ __forceinline__ void route_weights(const RouteArgs &a, const void *row, const int *sel, int sub, bool bad,
                                               float m, float sum, int32_t *ids, float *w, bool store) {
     const float inf = __builtin_huge_valf();
-    float top = -inf;
-    for (int j = sub; j < a.k; j += L) top = fmaxf(top, logit_at<TYPE>(row, sel[j]));
+    // k <= L in earnest: a lane's first logit stays in a register
+    const int id0 = sub < a.k ? sel[sub] : 0;
+    const float z0 = logit_at<TYPE>(row, id0);
+    float top = sub < a.k ? z0 : -inf;
+    for (int j = sub + L; j < a.k; j += L) top = fmaxf(top, logit_at<TYPE>(row, sel[j]));
     top = lanes_max<L>(top);
     const float least = a.sigmoid ? -709.0f : m - 745.0f;
     const bool nothing = !(top >= least) || top == -inf;
@@ -201,22 +247,23 @@ __device__ __forceinline__ void route_weights(const RouteArgs &a, const void *ro
         if (z >= 0.0f) return 1.0f / (1.0f + expf(-z));
         return expf(a.renorm ? z - ref : z) / (1.0f + expf(z));
     };
-    float S = 0.0f;
+    const float s0 = score(z0);
+    float S = a.sigmoid ? 1.0f : sum;
     if (a.renorm) {
-        for (int j = sub; j < a.k; j += L) S += score(logit_at<TYPE>(row, sel[j]));
+        S = sub < a.k ? s0 : 0.0f;
+        for (int j = sub + L; j < a.k; j += L) S += score(logit_at<TYPE>(row, sel[j]));
         S = lanes_sum<L>(S);
-    } else {
-        S = a.sigmoid ? 1.0f : sum;
     }
-    for (int j = sub; j < a.k; j += L) {
-        const int id = sel[j];
-        float v = nothing ? 0.0f : score(logit_at<TYPE>(row, id)) / S * a.scale;
+    const auto put = [&](int j, int id, float s) {
+        float v = nothing ? 0.0f : s / S * a.scale;
         if (bad) v = __builtin_nanf("");
         if (store) {
             ids[j] = id;
             w[j] = v;
         }
-    }
+    };
+    if (sub < a.k) put(sub, id0, s0);
+    for (int j = sub + L; j < a.k; j += L) put(j, sel[j], score(logit_at<TYPE>(row, sel[j])));
 }
 
 // m and sum of a whole row by one wave, as route_weights wants them.
@@ -258,9 +305,13 @@ __global__ __launch_bounds__(256) void k_moe_route_exact(const RouteArgs a) {
     }
 }
 
-// Doubles of LDS a wave needs.
+constexpr int kCands = 80;  // candidates of a token that are put in order at most
+
+// Doubles of LDS a wave needs: the exact keys of one token or of its tokens'
+// candidates, or its tokens' fp32 keys.
 __host__ __device__ inline int route_keys(int E, int tokens, int groups) {
-    return groups > 1 && tokens > 2 ? (E * tokens + 1) / 2 : E;
+    const int a = E > kCands * tokens ? E : kCands * tokens, b = groups > 1 ? (E * tokens + 1) / 2 : 0;
+    return a > b ? a : b;
 }
 
 // L lanes per token, V logits per lane (blocks of 4 neighbours, L blocks
@@ -272,18 +323,21 @@ __host__ __device__ inline int route_keys(int E, int tokens, int groups) {
 //     logits leave 13 bits for the whole id, and ties are decided; fp32
 //     logits lose 4 bits to the place in the lane
 //   else  keys in fp32, whose distance from the exact ones is bounded
-// A token in which two neighbours of the k + 1 best (or the groups at the
-// border) are nearer than what was lost is done again by route_exact: the
-// result is always the defined one. Moves E logits per token; bound by the
-// VALU work of the sort and the rounds.
+// Where two neighbours are nearer than what was lost, the rounds go on past k
+// until the gap behind the last is wide enough, and the candidates so far are
+// put in order by their exact keys. Groups too near each other at their border
+// (and more than kCands candidates) leave the token to route_exact: the result
+// is always the defined one. Moves E logits per token; bound by the VALU work
+// of the sort and the rounds.
 template <int TYPE, int L, int V, bool BY_LOGIT>
-__global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) {
+__global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, int64_t block0) {
     constexpr bool kIds = BY_LOGIT && TYPE != A2AV_DT_F32;   // whole ids in the keys
     constexpr uint32_t kLow = kIds ? 0x1fff : V - 1;
     constexpr int kTokens = kWave / L, kWaves = 4;
     extern __shared__ double keys[];  // a wave's exact keys of one token, or its tokens' fp32 keys
-    __shared__ uint32_t sorted[kWaves][V][kWave];
-    __shared__ int sel[kWaves][kTokens][kWave];
+    constexpr int kSorted = V * kWave > kTokens * kCands ? V : (kTokens * kCands + kWave - 1) / kWave;
+    __shared__ uint32_t sorted[kWaves][kSorted][kWave];      // or the candidates in order
+    __shared__ int sel[kWaves][kTokens][kCands];
     if (status_at_entry(a.status)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int sub = lane & (L - 1), mine = lane / L;
@@ -294,7 +348,10 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
     const int64_t n = (int64_t)a.W * a.T;
     const bool full = !a.sigmoid && (!BY_LOGIT || !a.renorm);  // needs the softmax's sum
     const uint64_t my_lanes = L == 64 ? ~0ull : 0xffffull << (lane & 48);
-    for (int64_t i0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens; i0 < n; i0 += (int64_t)gridDim.x * kWaves * kTokens) {
+    // no loop over tokens: the compiler would keep the constants of the double
+    // exponentials in registers across it
+    const int64_t i0 = (block0 + (int64_t)blockIdx.x) * (kWaves * kTokens) + wave * kTokens;
+    if (i0 < n) {
         const bool store = i0 + mine < n;
         const int64_t i = store ? i0 + mine : n - 1;
         const int r = (int)(i / a.T);
@@ -302,32 +359,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
         const void *row = logit_row<TYPE>(a.z[r], t, E);
         float z[V];
         int bad = 0;
-        if (vec) {
-#pragma unroll
-            for (int c = 0; c < V / 4; c++) {
-                const int e = (c * L + sub) * 4;
-                if constexpr (TYPE == A2AV_DT_F32) {
-                    f32x4 v = {-inf, -inf, -inf, -inf};
-                    if (e < E) v = *(const f32x4 *)((const float *)row + e);
-#pragma unroll
-                    for (int q = 0; q < 4; q++) z[c * 4 + q] = v[q];
-                } else {
-                    u32x2 v = {0, 0};
-                    if (e < E) v = *(const u32x2 *)((const uint16_t *)row + e);
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const uint16_t h = (uint16_t)(v[q / 2] >> (q % 2 * 16));
-                        z[c * 4 + q] = e < E ? logit_at<TYPE>(&h, 0) : -inf;
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int e = ((v / 4) * L + sub) * 4 + v % 4;
-                z[v] = e < E ? logit_at<TYPE>(row, e) : -inf;
-            }
-        }
+        load_logits<TYPE, L, V>(row, E, sub, vec, z);
         float m = -inf;
 #pragma unroll
         for (int v = 0; v < V; v++) {
@@ -351,10 +383,10 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
             for (int v = 0; v < V; v++) c[v] = z[v];
         } else {
             // sigmoid: the exponential's relative error is |z| 2^-23 at most and
-            // s (1 - s) |z| < 0.23, with a step each of the sum and the
-            // reciprocal under 2^-21 in all; softmax: a step for every term of
+            // s (1 - s) |z| < 0.23, with a step each of the exponential, the sum
+            // and the reciprocal 0.23 + 0.25 + 1 + 1 steps of 2^-23; softmax: a step for every term of
             // the sum and a few more, relative to at most 1 / sum
-            key_err = a.sigmoid ? 0x1p-20f : (V + 40) * 0x1p-23f / sum;
+            key_err = a.sigmoid ? 0x1p-21f : (V + 40) * 0x1p-23f / sum;
             const float scale = a.sigmoid ? 0.0f : 1.0f / sum;
 #pragma unroll
             for (int v = 0; v < V; v++) {
@@ -364,7 +396,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
                 c[v] = z[v] == -inf || s != s ? -inf : s;
             }
         }
-        bool unsure = false;
+        bool unsure = false;  // of the groups
         uint32_t kept = ~0u;
         if (a.groups > 1) {
             const int per = E / a.groups;
@@ -378,6 +410,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
             float t1 = -inf, t2 = -inf;
             if (sub < a.groups) {
                 int at = sub % per;  // the lanes start at different banks
+#pragma unroll 8
                 for (int q = 0; q < per; q++) {
                     const float x = group_keys[sub * per + at];
                     t2 = fmaxf(t2, fminf(t1, x));
@@ -431,40 +464,108 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec) 
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         uint32_t head = s[0], last = 0;
-        int at = 0;
-        const int rounds = k < E ? k + 1 : k;  // one more: the border
-        for (int j = 0; j < rounds; j++) {
+        int at = 0, count = 0;
+        bool mixed = false, closed = false;  // two candidates too near each other; the last one found
+        const uint64_t below = (1ull << lane) - 1;
+        for (int j = 0; j < kCands; j++) {
             const uint32_t top = lanes_max_u32<L>(head);
+            bool near = false;
             if constexpr (!kIds) {
-                if (j > 0) {
-                    if constexpr (BY_LOGIT) {
-                        unsure |= (top & ~kLow) == (last & ~kLow);
-                    } else if (top != 0) {  // 0: no expert is left
-                        const uint32_t x = last & ~kLow, y = top & ~kLow;
-                        const float hi = __uint_as_float(x ^ ((int)x < 0 ? 0x80000000u : 0xffffffffu));
-                        const float lo = __uint_as_float(y ^ ((int)y < 0 ? 0x80000000u : 0xffffffffu));
-                        unsure |= !(hi - lo > 2 * key_err + 0x1p-18f * fmaxf(fabsf(hi), fabsf(lo)));
-                    }
+                if (BY_LOGIT) {
+                    near = (top & ~kLow) == (last & ~kLow);
+                } else {
+                    // what the low bits hid is under 2^-19 of a key
+                    const uint32_t x = last & ~kLow, y = top & ~kLow;
+                    const float hi = __uint_as_float(x ^ ((int)x < 0 ? 0x80000000u : 0xffffffffu));
+                    const float lo = __uint_as_float(y ^ ((int)y < 0 ? 0x80000000u : 0xffffffffu));
+                    near = !(hi - lo > 2 * key_err + 0x1.01p-19f * fmaxf(fabsf(hi), fabsf(lo)));
                 }
+                near = near && j > 0;
                 last = top;
             }
-            const bool win = head == top;
-            if constexpr (!kIds) {  // the same key in two lanes
-                const uint64_t won = __ballot(win) & my_lanes;
-                unsure |= top != 0 && (won & (won - 1)) != 0;
+            near = near && top != 0;  // 0: no expert is left
+            closed = closed || (j >= k && !near);
+            if (__ballot(!closed) == 0) break;
+            if (!closed) {
+                mixed |= near;
+                count = j + 1;
             }
-            if (win && j < k) {
+            // of equal heads the first lane's goes
+            const bool top_head = head == top && !closed;
+            const uint64_t won = __ballot(top_head) & my_lanes;
+            if (top_head && (won & below) == 0) {
                 const int v = (int)(kLow - (top & kLow));
                 sel[wave][mine][j] = kIds ? v : ((v / 4) * L + sub) * 4 + v % 4;
+                at++;
+                head = at < V ? sorted[wave][at][lane] : 0;
             }
-            at += win;
-            if (win) head = at < V ? sorted[wave][at][lane] : 0;
         }
+        if constexpr (kIds) unsure = false;
+        else unsure |= !closed;  // more candidates than there is room for
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (is_bad || !store) {
             for (int j = sub; j < k; j += L) sel[wave][mine][j] = j;
-            unsure = false;
+            unsure = mixed = false;
+        }
+        mixed = mixed && !unsure;
+        if (!kIds && __ballot(mixed) != 0) {
+            // loops that keep nothing in registers: this is seldom reached, and
+            // its registers would cost every wave
+            double total = 1.0;
+            if (!BY_LOGIT && !a.sigmoid) {
+                total = 0.0;
+#pragma unroll 1
+                for (int e = sub; e < E; e += L) {
+                    const float x = logit_at<TYPE>(row, e);
+                    if (x != -inf) total += exp((double)x - m);
+                }
+#pragma unroll 1
+                for (int o = L / 2; o; o >>= 1) total += __shfl_xor(total, o);
+            }
+            double *mine_key = key + mine * kCands;
+            int *ids = sel[wave][mine], *in_order = (int *)&sorted[wave][0][0] + mine * kCands;
+            if (mixed) {
+#pragma unroll 1
+                for (int j = sub; j < count; j += L) {
+                    const double x = logit_at<TYPE>(row, ids[j]);
+                    double y = x;
+                    if (!BY_LOGIT) {
+                        y = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / total;
+                        if (a.bias) y += a.bias[ids[j]];
+                        if (x == -inf || y != y) y = -inf;
+                    }
+                    mine_key[j] = y;
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (mixed) {
+#pragma unroll 1
+                for (int j = sub; j < count; j += L) {
+                    const double y = mine_key[j];
+                    const int id = ids[j];
+                    int rank = 0;
+#pragma unroll 1
+                    for (int q = 0; q < count; q++) {
+                        const double o = mine_key[q];
+                        bool first = o > y;
+                        if (o == y && q != j) {
+                            const int oid = ids[q];
+                            const float x = logit_at<TYPE>(row, id), ox = logit_at<TYPE>(row, oid);
+                            first = ox > x || (ox == x && oid < id);
+                        }
+                        rank += first;
+                    }
+                    in_order[rank] = id;
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (mixed)
+                for (int j = sub; j < k; j += L) ids[j] = in_order[j];
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
         // tokens to do again, one after the other, by the whole wave
         uint64_t again = __ballot(unsure && sub == 0);
@@ -530,7 +631,7 @@ __device__ __forceinline__ void store_logit(void *row, int64_t i, float v) {
 // out of the weights, so that s_j / S is w_j / scale), and every lane adds up
 // what falls on its experts, in slot order.
 template <int TYPE>
-__global__ __launch_bounds__(256) void k_moe_route_backward(const RouteGradArgs a) {
+__global__ __launch_bounds__(256) void k_moe_route_backward_any(const RouteGradArgs a) {
     if (status_at_entry(a.status)) return;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int waves = blockDim.x / kWave;
@@ -577,6 +678,113 @@ __global__ __launch_bounds__(256) void k_moe_route_backward(const RouteGradArgs 
     }
 }
 
+// L lanes per token, V logits per lane, as k_moe_route. Lane j holds ds_j * s_j
+// of chosen expert j; the first of equal ids collects their sum (in slot
+// order), so that the row's gradients meet in LDS without atomics. Writes E
+// values per token and reads them where softmax is not renormalised; bound by
+// those bytes.
+template <int TYPE, int L, int V>
+__global__ __launch_bounds__(256) void k_moe_route_backward(const RouteGradArgs a, bool vec) {
+    constexpr int kTokens = kWave / L, kWaves = 4;
+    __shared__ __align__(16) float rows[kWaves][kTokens][L * V];
+    __shared__ int ids[kWaves][kTokens][kWave];
+    __shared__ float vals[kWaves][kTokens][kWave];
+    if (status_at_entry(a.status)) return;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int sub = lane & (L - 1), mine = lane / L;
+    const int E = a.E, k = a.k;
+    const float inf = __builtin_huge_valf();
+    const int64_t n = (int64_t)a.W * a.T;
+    const bool full = !a.sigmoid && !a.renorm;
+    float *d = rows[wave][mine], *val = vals[wave][mine];
+    int *id = ids[wave][mine];
+    for (int64_t i0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens; i0 < n; i0 += (int64_t)gridDim.x * kWaves * kTokens) {
+        const bool store = i0 + mine < n;
+        const int64_t i = store ? i0 + mine : n - 1;
+        const int r = (int)(i / a.T);
+        const int64_t t = i - (int64_t)r * a.T;
+        const void *row = logit_row<TYPE>(a.z[r], t, E);
+        void *out = (void *)logit_row<TYPE>(a.dz[r], t, E);
+        float z[V];
+        if (full) {
+            load_logits<TYPE, L, V>(row, E, sub, vec, z);
+        }
+        float dot = 0.0f;
+        for (int j = sub; j < k; j += L) dot += a.dw[r][t * k + j] * a.w[r][t * k + j];
+        dot = lanes_sum<L>(dot);
+        for (int j = sub; j < k; j += L) {
+            const int e = a.ids[r][t * k + j];
+            const float w = a.w[r][t * k + j], g = a.dw[r][t * k + j];
+            float v = w * g;
+            if (a.renorm) v = a.scale == 0 ? 0.0f : w * (g - dot / a.scale);
+            if (a.sigmoid) v *= 1.0f / (1.0f + expf(logit_at<TYPE>(row, e)));
+            id[j] = e;
+            val[j] = v;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v += 4) *(f32x4 *)(d + (v / 4 * L + sub) * 4) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int j = sub; j < k; j += L) {
+            float v = 0.0f;
+            bool first = true;
+            const int e = id[j];
+            for (int q = 0; q < k; q++) {
+                const bool same = id[q] == e;
+                first = first && !(same && q < j);
+                v += same ? val[q] : 0.0f;
+            }
+            if (first) d[e] = v;
+        }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float f = 0.0f;
+        if (full) {
+            float m = -inf, sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; v++) m = fmaxf(m, z[v]);
+            m = lanes_max<L>(m);
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                // a row of -inf has no gradient; NaN passes on
+                z[v] = z[v] == -inf ? 0.0f : __expf(z[v] - m);
+                sum += z[v];
+            }
+            sum = lanes_sum<L>(sum);
+            f = sum == 0.0f ? 0.0f : dot / sum;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const int e = (v / 4 * L + sub) * 4;
+            f32x4 y = *(const f32x4 *)(d + e);
+            if (full) {
+#pragma unroll
+                for (int q = 0; q < 4; q++) y[q] -= f * z[v + q];
+            }
+            if (!store) continue;
+            if (vec) {
+                if (e < E) {
+                    if constexpr (TYPE == A2AV_DT_F32) {
+                        *(f32x4 *)((float *)out + e) = y;
+                    } else {
+                        uint16_t h[4];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) store_logit<TYPE>(h, q, y[q]);
+                        u32x2 o;
+                        o.x = h[0] | (uint32_t)h[1] << 16;
+                        o.y = h[2] | (uint32_t)h[3] << 16;
+                        *(u32x2 *)((uint16_t *)out + e) = o;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    if (e + q < E) store_logit<TYPE>(out, e + q, y[q]);
+            }
+        }
+    }
+}
+
 static bool route_sizes_ok(int W, int64_t T, int k, int E, int type, int score) {
     if (W < 1 || W > A2AV_MAX_W || T < 0 || k < 1 || k > kWave || E < 1 || E > A2AV_MAX_EXPERTS) return false;
     if (type < A2AV_DT_F32 || type > A2AV_DT_F16) return false;
@@ -592,10 +800,13 @@ static unsigned wave_grid(int64_t waves, int per_block) {
 
 template <int TYPE, int L, int V>
 static void launch_route(const RouteArgs &a, bool by_logit, bool vec, hipStream_t stream) {
-    const unsigned blocks = wave_grid(((int64_t)a.W * a.T * L + kWave - 1) / kWave, 4);
+    const int64_t tokens = 4 * kWave / L, all = ((int64_t)a.W * a.T + tokens - 1) / tokens;
     const unsigned lds = (unsigned)(4 * route_keys(a.E, kWave / L, a.groups) * sizeof(double));
-    if (by_logit) hipLaunchKernelGGL((k_moe_route<TYPE, L, V, true>), dim3(blocks), dim3(256), lds, stream, a, vec);
-    else hipLaunchKernelGGL((k_moe_route<TYPE, L, V, false>), dim3(blocks), dim3(256), lds, stream, a, vec);
+    for (int64_t b = 0; b < all; b += max_grid()) {
+        const dim3 g((unsigned)(all - b < max_grid() ? all - b : max_grid()));
+        if (by_logit) hipLaunchKernelGGL((k_moe_route<TYPE, L, V, true>), g, dim3(256), lds, stream, a, vec, b);
+        else hipLaunchKernelGGL((k_moe_route<TYPE, L, V, false>), g, dim3(256), lds, stream, a, vec, b);
+    }
 }
 
 template <int TYPE>
@@ -615,6 +826,28 @@ static void launch_route(const RouteArgs &a, bool vec, hipStream_t stream) {
         launch_route<TYPE, 16, 16>(a, by_logit, vec, stream);
     } else {
         launch_route<TYPE, 64, 16>(a, by_logit, vec, stream);
+    }
+}
+
+template <int TYPE, int L, int V>
+static void launch_route_backward(const RouteGradArgs &a, bool vec, hipStream_t stream) {
+    const unsigned blocks = wave_grid(((int64_t)a.W * a.T * L + kWave - 1) / kWave, 4);
+    hipLaunchKernelGGL((k_moe_route_backward<TYPE, L, V>), dim3(blocks), dim3(256), 0, stream, a, vec);
+}
+
+template <int TYPE>
+static void launch_route_backward(const RouteGradArgs &a, bool vec, hipStream_t stream) {
+    if (a.E > 1024) {
+        const unsigned blocks = wave_grid((int64_t)a.W * a.T, 4);
+        hipLaunchKernelGGL(k_moe_route_backward_any<TYPE>, dim3(blocks), dim3(256), 0, stream, a);
+    } else if (a.E <= 64) {
+        launch_route_backward<TYPE, 16, 4>(a, vec, stream);
+    } else if (a.E <= 128) {
+        launch_route_backward<TYPE, 16, 8>(a, vec, stream);
+    } else if (a.E <= 256) {
+        launch_route_backward<TYPE, 16, 16>(a, vec, stream);
+    } else {
+        launch_route_backward<TYPE, 64, 16>(a, vec, stream);
     }
 }
 
@@ -692,11 +925,13 @@ A2AV_API int moe_route_backward(int W, int64_t T, int k, int E, int type, int sc
     a.scale = scale;
     if (T == 0) return A2AV_OK;
     hipLaunchKernelGGL(k_route_check, dim3((unsigned)((T * k + 255) / 256), W), dim3(256), 0, stream, a);
-    const unsigned blocks = wave_grid((int64_t)W * T, 4);
+    bool vec = E % 4 == 0;
+    for (int r = 0; r < W; r++)
+        vec = vec && (uintptr_t)logits[r] % 16 == 0 && (uintptr_t)d_logits[r] % 16 == 0;
     switch (type) {
-    case A2AV_DT_F32: hipLaunchKernelGGL(k_moe_route_backward<A2AV_DT_F32>, dim3(blocks), dim3(256), 0, stream, a); break;
-    case A2AV_DT_BF16: hipLaunchKernelGGL(k_moe_route_backward<A2AV_DT_BF16>, dim3(blocks), dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL(k_moe_route_backward<A2AV_DT_F16>, dim3(blocks), dim3(256), 0, stream, a); break;
+    case A2AV_DT_F32: launch_route_backward<A2AV_DT_F32>(a, vec, stream); break;
+    case A2AV_DT_BF16: launch_route_backward<A2AV_DT_BF16>(a, vec, stream); break;
+    default: launch_route_backward<A2AV_DT_F16>(a, vec, stream); break;
     }
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

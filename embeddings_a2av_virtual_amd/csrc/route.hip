@@ -309,9 +309,10 @@ constexpr int kCands = 80;  // candidates of a token that are put in order at mo
 
 // Doubles of LDS a wave needs: the exact keys of one token or of its tokens'
 // candidates, or its tokens' fp32 keys.
-__host__ __device__ inline int route_keys(int E, int tokens, int groups) {
-    const int a = E > kCands * tokens ? E : kCands * tokens, b = groups > 1 ? (E * tokens + 1) / 2 : 0;
-    return a > b ? a : b;
+__host__ __device__ inline int route_keys(int E, int tokens, int keys) {
+    const int a = E > kCands * tokens ? E : kCands * tokens, b = keys * tokens / 2;
+    const int c = a > b ? a : b;
+    return c + (c & 1);  // 16-byte multiples
 }
 
 // L lanes per token, V logits per lane (blocks of 4 neighbours, L blocks
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
     constexpr bool kIds = BY_LOGIT && TYPE != A2AV_DT_F32;   // whole ids in the keys
     constexpr uint32_t kLow = kIds ? 0x1fff : V - 1;
     constexpr int kTokens = kWave / L, kWaves = 4;
-    extern __shared__ double keys[];  // a wave's exact keys of one token, or its tokens' fp32 keys
+    extern __shared__ __align__(16) double keys[];  // a wave's exact keys of one token, or its tokens' fp32 keys
     constexpr int kSorted = V * kWave > kTokens * kCands ? V : (kTokens * kCands + kWave - 1) / kWave;
     __shared__ uint32_t sorted[kWaves][kSorted][kWave];      // or the candidates in order
     __shared__ int sel[kWaves][kTokens][kCands];
@@ -343,8 +344,8 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
     const int sub = lane & (L - 1), mine = lane / L;
     const int E = a.E, k = a.k;
     const float inf = __builtin_huge_valf();
-    double *key = keys + (size_t)wave * route_keys(E, kTokens, a.groups);
-    float *group_keys = (float *)key + mine * E;
+    double *key = keys + (size_t)wave * route_keys(E, kTokens, a.groups > 1 ? L * V : 0);
+    float *group_keys = (float *)key + mine * (L * V);
     const int64_t n = (int64_t)a.W * a.T;
     const bool full = !a.sigmoid && (!BY_LOGIT || !a.renorm);  // needs the softmax's sum
     const uint64_t my_lanes = L == 64 ? ~0ull : 0xffffull << (lane & 48);
@@ -387,24 +388,30 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
             // and the reciprocal 0.23 + 0.25 + 1 + 1 steps of 2^-23; softmax: a step for every term of
             // the sum and a few more, relative to at most 1 / sum
             key_err = a.sigmoid ? 0x1p-21f : (V + 40) * 0x1p-23f / sum;
-            const float scale = a.sigmoid ? 0.0f : 1.0f / sum;
+            if (a.sigmoid) {
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int e = ((v / 4) * L + sub) * 4 + v % 4;
-                float s = a.sigmoid ? 1.0f / (1.0f + __expf(-z[v])) : c[v] * scale;
-                if (a.bias && e < E) s += a.bias[e];
-                c[v] = z[v] == -inf || s != s ? -inf : s;
+                for (int v = 0; v < V; v++) c[v] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[v]));
+            } else {
+                const float scale = 1.0f / sum;
+#pragma unroll
+                for (int v = 0; v < V; v++) c[v] *= scale;
             }
+            if (a.bias) {
+                float b[V];
+                load_logits<A2AV_DT_F32, L, V>(a.bias, E, sub, vec, b);
+#pragma unroll
+                for (int v = 0; v < V; v++) c[v] += b[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; v++) c[v] = z[v] == -inf || c[v] != c[v] ? -inf : c[v];
         }
         bool unsure = false;  // of the groups
         uint32_t kept = ~0u;
         if (a.groups > 1) {
             const int per = E / a.groups;
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int e = ((v / 4) * L + sub) * 4 + v % 4;
-                if (e < E) group_keys[e] = c[v];
-            }
+            for (int v = 0; v < V; v += 4)
+                *(f32x4 *)(group_keys + (v / 4 * L + sub) * 4) = f32x4{c[v], c[v + 1], c[v + 2], c[v + 3]};
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             float t1 = -inf, t2 = -inf;
@@ -421,6 +428,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
             float gs = a.group_top == 1 ? t1 : t1 + t2;
             if (gs != gs) gs = -inf;
             int before = 0;
+#pragma unroll 4
             for (int g = 0; g < a.groups; g++) {
                 const float o = __shfl(gs, g, L);
                 before += o > gs || (o == gs && g < sub);
@@ -801,7 +809,7 @@ static unsigned wave_grid(int64_t waves, int per_block) {
 template <int TYPE, int L, int V>
 static void launch_route(const RouteArgs &a, bool by_logit, bool vec, hipStream_t stream) {
     const int64_t tokens = 4 * kWave / L, all = ((int64_t)a.W * a.T + tokens - 1) / tokens;
-    const unsigned lds = (unsigned)(4 * route_keys(a.E, kWave / L, a.groups) * sizeof(double));
+    const unsigned lds = (unsigned)(4 * route_keys(a.E, kWave / L, a.groups > 1 ? L * V : 0) * sizeof(double));
     for (int64_t b = 0; b < all; b += max_grid()) {
         const dim3 g((unsigned)(all - b < max_grid() ? all - b : max_grid()));
         if (by_logit) hipLaunchKernelGGL((k_moe_route<TYPE, L, V, true>), g, dim3(256), lds, stream, a, vec, b);
@@ -886,7 +894,7 @@ A2AV_API int moe_route(int W, int64_t T, int k, int E, int type, int score,
     a.renorm = renorm != 0;
     a.scale = scale;
     if (T == 0) return A2AV_OK;
-    bool vec = E % 4 == 0;
+    bool vec = E % 4 == 0 && (uintptr_t)bias % 16 == 0;
     for (int r = 0; r < W; r++) vec = vec && (uintptr_t)logits[r] % 16 == 0;
     switch (type) {
     case A2AV_DT_F32: launch_route<A2AV_DT_F32>(a, vec, stream); break;

@@ -886,6 +886,7 @@ __global__ __launch_bounds__(256) void k_expert_few(const ExpertArgs a) {
 
 // ------------------------------------------------------------------ d_pre and the bias
 constexpr int kBlockRows = 64;  // rows of a block of the bias sums
+constexpr int kVecCols = 64;    // columns of a workgroup of the 16-byte form
 
 struct DpreArgs {
     const void *pre[A2AV_MAX_W];
@@ -915,11 +916,11 @@ __device__ __forceinline__ void dpre_of(int act, float g, float h, float up, flo
     }
 }
 
-// One workgroup per (row block, 256 output columns). VEC: a thread has 8
-// neighbouring columns of every eighth row (16-byte loads and stores, four
-// rows in flight), and the eight rows' sums meet in LDS in a fixed order;
-// otherwise a thread walks one column down the block's rows. Bound by the
-// bytes: it reads and writes what it has to once.
+// One workgroup per row block and 64 output columns (VEC) or 256. VEC: a
+// thread has 8 neighbouring columns of two rows (16-byte loads and stores, all
+// of them in flight together), and the rows' sums meet in LDS in a fixed
+// order; otherwise a thread walks one column down the block's rows. Bound by
+// the bytes, which it reads and writes once.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
     if (status_at_entry(a.status)) return;
@@ -937,38 +938,36 @@ __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
     const uint16_t *d_out = (const uint16_t *)a.d_out[d], *pre = (const uint16_t *)a.pre[d];
     uint16_t *d_pre = (uint16_t *)a.d_pre[d];
     if constexpr (VEC) {
-        __shared__ float part[2][8][256];
-        const int col = threadIdx.x % 32, group = threadIdx.x / 32;
-        const int64_t n = (int64_t)blockIdx.x * 256 + col * 8;
+        constexpr int kLanes = kVecCols / 8, kGroups = 256 / kLanes, kRows = kBlockRows / kGroups;
+        __shared__ float part[2][kGroups][kVecCols];
+        const int col = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+        const int64_t n = (int64_t)blockIdx.x * kVecCols + col * 8, r = r0 + group;
         float s0[8] = {}, s1[8] = {};
-        constexpr int kRows = 4;
-        if (n < a.N) {
-            for (int64_t r = r0 + group; r < r1; r += 8 * kRows) {
-                u16x8 g[kRows], h[kRows], up[kRows];
+        if (n < a.N && r < r1) {
+            u16x8 g[kRows], h[kRows], up[kRows];
 #pragma unroll
-                for (int i = 0; i < kRows; i++) {
-                    const int64_t row = r + i * 8 < r1 ? r + i * 8 : r;  // past the block: row r again, not used
-                    g[i] = *(const u16x8 *)(d_out + row * a.N + n);
-                    if (!none) h[i] = *(const u16x8 *)(pre + row * a.NW + n);
-                    if (glu) up[i] = *(const u16x8 *)(pre + row * a.NW + a.N + n);
+            for (int i = 0; i < kRows; i++) {
+                const int64_t row = r + i * kGroups < r1 ? r + i * kGroups : r;  // past the block: row r again, not used
+                g[i] = *(const u16x8 *)(d_out + row * a.N + n);
+                if (!none) h[i] = *(const u16x8 *)(pre + row * a.NW + n);
+                if (glu) up[i] = *(const u16x8 *)(pre + row * a.NW + a.N + n);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; i++) {
+                const int64_t row = r + i * kGroups;
+                if (row >= r1) break;
+                float dh[8], du[8];
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    dh[c] = T::to_float(g[i][c]);
+                    du[c] = 0.0f;
+                    if (!none)
+                        dpre_of(act, dh[c], T::to_float(h[i][c]), glu ? T::to_float(up[i][c]) : 0.0f, dh[c], du[c]);
+                    s0[c] += dh[c];
+                    s1[c] += du[c];
                 }
-#pragma unroll
-                for (int i = 0; i < kRows; i++) {
-                    const int64_t row = r + i * 8;
-                    if (row >= r1) break;
-                    float dh[8], du[8];
-#pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        dh[c] = T::to_float(g[i][c]);
-                        du[c] = 0.0f;
-                        if (!none)
-                            dpre_of(act, dh[c], T::to_float(h[i][c]), glu ? T::to_float(up[i][c]) : 0.0f, dh[c], du[c]);
-                        s0[c] += dh[c];
-                        s1[c] += du[c];
-                    }
-                    if (!none) put8<T>(d_pre + row * a.NW + n, dh);
-                    if (glu) put8<T>(d_pre + row * a.NW + a.N + n, du);
-                }
+                if (!none) put8<T>(d_pre + row * a.NW + n, dh);
+                if (glu) put8<T>(d_pre + row * a.NW + a.N + n, du);
             }
         }
         if (!a.has_bias) return;
@@ -978,11 +977,11 @@ __global__ __launch_bounds__(256) void k_expert_dpre(const DpreArgs a) {
             part[1][group][col * 8 + c] = s1[c];
         }
         __syncthreads();
-        const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        if (m >= a.N) return;
+        const int64_t m = (int64_t)blockIdx.x * kVecCols + threadIdx.x;
+        if (threadIdx.x >= kVecCols || m >= a.N) return;
         float x = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
+#pragma unroll 8
+        for (int i = 0; i < kGroups; i++) {
             x += part[0][i][threadIdx.x];
             y += part[1][i][threadIdx.x];
         }
@@ -1035,7 +1034,7 @@ static int64_t tile_bound(int W, int P, int64_t K, int64_t N, int act, const int
     if (K > A2AV_MAX_WIDTH || N > A2AV_MAX_WIDTH) return -1;
     int64_t total = 0;
     for (int d = 0; d < W; d++) {
-        if (x_rows[d] < 0 || x_rows[d] > ((int64_t)1 << 40)) return -1;
+        if (x_rows[d] < 0 || x_rows[d] > ((int64_t)1 << 30)) return -1;
         total += x_rows[d];
     }
     const int64_t t = total / tile_rows + (int64_t)W * P;
@@ -1043,6 +1042,7 @@ static int64_t tile_bound(int W, int P, int64_t K, int64_t N, int act, const int
 }
 
 // Tile shapes of the fast products, largest first.
+constexpr int64_t kMostGroups = 1 << 22;  // workgroups of a launch, times 512 threads inside 32 bits
 enum { kBig, kMid, kSmall, kFew };
 constexpr int kTile[] = {256, 128, 64, kFewRows};
 constexpr int kMostBlocks = 4;  // row blocks of the largest tile
@@ -1101,8 +1101,9 @@ static dim3 tile_grid(int64_t columns, int64_t tiles) {
     return dim3((unsigned)columns, (unsigned)y, (unsigned)((tiles + y - 1) / y));
 }
 
+// False for more workgroups than a launch can have.
 template <int KIND, typename T>
-static void launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, hipStream_t stream) {
+static bool launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, hipStream_t stream) {
     const int64_t cols = KIND != kForward ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
     const int64_t t = fast ? kTile[shape] : kAny;
     a.cols = (int)((cols + t - 1) / t);
@@ -1110,29 +1111,33 @@ static void launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, h
     if (!fast) {
         const dim3 g = KIND == kDweight ? dim3(a.cols, a.row_tiles, a.W * a.P) : tile_grid(a.cols, tiles);
         hipLaunchKernelGGL((k_expert_any<KIND, T>), g, dim3(256), 0, stream, a);
-        return;
+        return true;
     }
     if constexpr (KIND == kForward) {
         if (shape == kFew) {
             a.cols = (int)((a.N + 15) / 16);
+            if (tiles * a.cols > kMostGroups) return false;
             const dim3 g((unsigned)(tiles * a.cols));
             if (a.act == A2AV_ACT_SWIGLU) hipLaunchKernelGGL((k_expert_few<T, true>), g, dim3(256), 0, stream, a);
             else hipLaunchKernelGGL((k_expert_few<T, false>), g, dim3(256), 0, stream, a);
-            return;
+            return true;
         }
     }
     if (KIND == kDweight) tiles = (int64_t)a.W * a.P * a.row_tiles;
+    if (tiles * a.cols > kMostGroups) return false;
     const dim3 g((unsigned)((tiles * a.cols + 7) / 8 * 8));
     if (shape == kBig) hipLaunchKernelGGL((k_expert_tile<KIND, T, 256, 256, 2, 4, 64>), g, dim3(512), 0, stream, a);
     else if (shape == kMid)
         hipLaunchKernelGGL((k_expert_tile<KIND, T, 128, 128, 2, 2, KIND == kDweight ? 32 : 64>), g, dim3(256), 0, stream, a);
-    else if (shape == kSmall) hipLaunchKernelGGL((k_expert_tile<KIND, T, 64, 64, 2, 2, 64>), g, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_expert_tile<KIND, T, 64, 64, 2, 2, 64>), g, dim3(256), 0, stream, a);
+    return true;
 }
 
 template <int KIND>
-static void launch_product(ExpertArgs &a, int type, int shape, bool fast, int64_t tiles, hipStream_t stream) {
-    if (type == A2AV_DT_BF16) launch_product<KIND, Bf16>(a, shape, fast, tiles, stream);
-    else launch_product<KIND, Fp16>(a, shape, fast, tiles, stream);
+static bool launch_product(ExpertArgs &a, int type, int shape, bool fast, int64_t tiles, hipStream_t stream) {
+    if (type == A2AV_DT_BF16) return launch_product<KIND, Bf16>(a, shape, fast, tiles, stream);
+    return launch_product<KIND, Fp16>(a, shape, fast, tiles, stream);
 }
 
 // Most tiles of `rows` rows that a product's row tiles can be.
@@ -1208,7 +1213,8 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     // against 44 at K 2048; 12 rows an expert at K 7168: 210 against 172 us.)
     const int shape = !fast ? kSmall : R <= 4 * n && K >= 4096 ? kFew : shape_of(R, n, 0, a.NW);
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], (unsigned char *)workspace, l, status, stream);
-    launch_product<kForward>(a, type, shape, fast, most_tiles(x_rows, W, P, kTile[shape]), stream);
+    if (!launch_product<kForward>(a, type, shape, fast, most_tiles(x_rows, W, P, kTile[shape]), stream))
+        return A2AV_EHIP;
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }
 
@@ -1279,7 +1285,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
     g.blocks = kTile[shape] / kBlockRows;
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], ws, l, status, stream);
     if (!none || d_bias) {
-        const dim3 grid = tile_grid((N + 255) / 256, tiles * g.blocks);
+        const dim3 grid = tile_grid(vec ? (N + kVecCols - 1) / kVecCols : (N + 255) / 256, tiles * g.blocks);
         if (type == A2AV_DT_BF16 && vec) hipLaunchKernelGGL((k_expert_dpre<Bf16, true>), grid, dim3(256), 0, stream, g);
         else if (type == A2AV_DT_BF16) hipLaunchKernelGGL((k_expert_dpre<Bf16, false>), grid, dim3(256), 0, stream, g);
         else if (vec) hipLaunchKernelGGL((k_expert_dpre<Fp16, true>), grid, dim3(256), 0, stream, g);
@@ -1290,7 +1296,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dbias<Bf16>, grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL(k_expert_dbias<Fp16>, grid, dim3(256), 0, stream, g);
     }
-    if (d_x) launch_product<kDx>(a, type, shape, fast, tiles, stream);
+    if (d_x && !launch_product<kDx>(a, type, shape, fast, tiles, stream)) return A2AV_EHIP;
         if (d_weight) {
         // Few rows an expert: the tile's sums are short and its stores long, and
         // four workgroups of the middle size on a compute unit cover the one
@@ -1298,7 +1304,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         // an expert, 1215 against 1206 at 512, 993 against 954 at 1024.)
         int s = fast ? shape_of(R, n, a.NW, K) : kSmall;
         if (s == kBig && R < 512 * n) s = kMid;
-        launch_product<kDweight>(b, type, s, fast, 0, stream);
+        if (!launch_product<kDweight>(b, type, s, fast, 0, stream)) return A2AV_EHIP;
     }
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

@@ -648,7 +648,7 @@ size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int
  * up rows, and act(h) = silu(h[0..N)) * h[N..2N). NW below is 2N then, else N.
  *   K, N            1 .. A2AV_MAX_WIDTH
  *   type            A2AV_DT_BF16 or A2AV_DT_F16, of every array
- *   x[W]            device [x_rows[d]][K] (host x_rows)
+ *   x[W]            device [x_rows[d]][K] (host x_rows, at most 2^30)
  *   expert_offsets  device int64 [W][P+1] (block_offsets / expert_offsets of
  *                   the calls above); W * P <= A2AV_MAX_EXPERTS
  *   weight[W]       device [P][NW][K]

@@ -353,6 +353,17 @@ __global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
 // Rows, columns and contraction steps outside are loaded out of the buffer's
 // range, which writes zeros to LDS; so the last steps can go on loading what
 // nobody reads, and every step waits for the same number of loads.
+//
+// What bounds it, at 16384 rows, K 7168 and 4096 columns in bf16 (one library
+// product of that size: 615-650 us): the matrix cores' power. The kernel needs
+// 1.16 M cycles of each compute unit and its clock falls to 1.5 GHz (767 us;
+// the library's product 1.05 M cycles at 1.6 GHz). Other shapes, same box, all
+// three products (forward / d_x / d_weight, us through): eight waves and two
+// stages of 64 with one barrier a step 848 / 849 / spills; two groups of waves
+// in turn at reading and multiplying 928 / 778 / 852; four stages of 32, whose
+// 64-byte requests double the L2's work, 920 / 834 / 755; four waves of 128 x
+// 128, half the LDS reads but no second wave to issue beside a stalled one,
+// 889 / 818 / 825; this one 875 / 811 / 808 and the fastest on ragged experts.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef __attribute__((address_space(3))) void lds_void;

@@ -818,9 +818,14 @@ __global__ __launch_bounds__(256) void k_mark_check(const CombineGradArgs a) {
 }
 
 // One workgroup per token; its waves take the token's slots in turn, so the
-// token's d_out comes from HBM once and from the L1 for the other slots.
-// Moves 2 * k + 1 rows per token and is bound by that traffic.
-template <bool HOME, bool ALIGNED>
+// token's d_out comes from HBM once and from the L1 for the other slots. Moves
+// 2 * k + 1 rows per token and is bound by that traffic: 2.0 GB in 378 us at 8
+// x 1024 tokens, 8 slots, H = 7168, 86 % of the rate of a plain copy. U: the
+// vectors a lane has in flight, as many as tile the row in the fewest steps (7
+// there; 388 us with 4, 402 with 14). Non-temporal on both sides (ordinary
+// loads or stores 390-406 us); LDS reserved to run fewer workgroups changed
+// nothing.
+template <bool HOME, bool ALIGNED, int U>
 __global__ __launch_bounds__(512) void k_combine_backward(const CombineGradArgs a) {
     if (status_at_entry(a.status)) return;
     if constexpr (HOME) {
@@ -858,7 +863,6 @@ __global__ __launch_bounds__(512) void k_combine_backward(const CombineGradArgs 
             float acc = 0.0f;
             if constexpr (ALIGNED) {
                 const uint64_t nv = rowb / 16;
-                constexpr int U = 4;
                 for (uint64_t i0 = 0; i0 < nv; i0 += U * kWave) {
                     u32x4 x[U], y[U];
 #pragma unroll
@@ -906,8 +910,21 @@ static void launch_combine_backward(const CombineGradArgs &a, bool aligned, hipS
     if (blocks < 1) blocks = 1;  // a verdict of the plan is reported
     if (blocks > max_grid()) blocks = max_grid();
     const dim3 g((unsigned)blocks), b(waves * kWave);
-    if (aligned) hipLaunchKernelGGL((k_combine_backward<HOME, true>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((k_combine_backward<HOME, false>), g, b, 0, stream, a);
+    if (!aligned) {
+        hipLaunchKernelGGL((k_combine_backward<HOME, false, 1>), g, b, 0, stream, a);
+        return;
+    }
+    const uint64_t nv = (uint64_t)a.H / 8, steps = (nv + 8 * kWave - 1) / (8 * kWave);
+    switch ((int)((nv + steps * kWave - 1) / (steps * kWave))) {
+    case 1: hipLaunchKernelGGL((k_combine_backward<HOME, true, 1>), g, b, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((k_combine_backward<HOME, true, 2>), g, b, 0, stream, a); break;
+    case 3: hipLaunchKernelGGL((k_combine_backward<HOME, true, 3>), g, b, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((k_combine_backward<HOME, true, 4>), g, b, 0, stream, a); break;
+    case 5: hipLaunchKernelGGL((k_combine_backward<HOME, true, 5>), g, b, 0, stream, a); break;
+    case 6: hipLaunchKernelGGL((k_combine_backward<HOME, true, 6>), g, b, 0, stream, a); break;
+    case 7: hipLaunchKernelGGL((k_combine_backward<HOME, true, 7>), g, b, 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_combine_backward<HOME, true, 8>), g, b, 0, stream, a); break;
+    }
 }
 
 static int64_t n_segments(int64_t Q) { return (Q + kSeg - 1) / kSeg; }

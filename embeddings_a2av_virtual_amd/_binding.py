@@ -195,6 +195,9 @@ def _i64_array(vals):
 
 
 _PTRS = [ctypes.c_void_p * n for n in range(MAX_W + 1)]
+_Tensor = torch.Tensor
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _typed(tensors, name, dtype, sizes):
@@ -205,15 +208,18 @@ def _typed(tensors, name, dtype, sizes):
     if len(tensors) != len(sizes):
         raise ValueError(f"{name} needs {len(sizes)} entries")
     ptrs = []
+    add = ptrs.append
     for t, n in zip(tensors, sizes):
-        # the usual case without a call per check; anything else is looked into
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
-            ptrs.append(t.data_ptr())
+        # the usual case in one expression; anything else is looked into
+        if (type(t) is _Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+                and t.numel() >= n):
+            add(t.data_ptr())
+        elif t is None:
+            if n > 0:
+                raise ValueError(f"{name}[{len(ptrs)}] needs {n} elements")
+            add(None)
         else:
-            i = len(ptrs)
-            if t is None and n > 0:
-                raise ValueError(f"{name}[{i}] needs {n} elements")
-            ptrs.append(None if t is None else _one(t, f"{name}[{i}]", dtype, n))
+            add(_one(t, f"{name}[{len(ptrs)}]", dtype, n))
     return _PTRS[len(ptrs)](*ptrs) if len(ptrs) <= MAX_W else (ctypes.c_void_p * len(ptrs))(*ptrs)
 
 
@@ -237,11 +243,12 @@ def _call(fn, like, stream, *args):
     current."""
     f = getattr(_lib or lib(), fn)
     device = like.device.index
+    s = _raw_stream(device) if stream is None and _raw_stream else _stream(stream, like)
     if device == torch.cuda.current_device():
-        rc = f(*args, _stream(stream, like))
+        rc = f(*args, s)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, _stream(stream, like))
+            rc = f(*args, s)
     if rc != OK:
         raise A2avError(fn, rc)
 
@@ -475,8 +482,8 @@ def moe_route_backward(W, T, k, E, score, logits, ids, weights, renorm, scale, d
                        status, stream=None):
     """The gradient of moe_route's weights in its logits, the ids held fixed."""
     dtype = _logits_type(logits)
-    _call("moe_route_backward", status, stream, int(W), int(T), int(k), int(E), _TYPES[dtype], int(score),
-          _typed(logits, "logits", dtype, [T * E] * W),
+    _call("moe_route_backward", status, stream, int(W), int(T), int(k), int(E), _TYPES[dtype],
+          int(score), _typed(logits, "logits", dtype, [T * E] * W),
           _typed(ids, "ids", torch.int32, [T * k] * W),
           _typed(weights, "weights", torch.float32, [T * k] * W), int(bool(renorm)), float(scale),
           _typed(d_weights, "d_weights", torch.float32, [T * k] * W),
@@ -553,8 +560,8 @@ def moe_expert_linear(W, P, K, N, act, x, x_rows, expert_offsets, weight, bias, 
     if len(x_rows) != W:
         raise ValueError("x_rows needs W entries")
     narrow, wide = [int(n) * N for n in x_rows], [int(n) * NW for n in x_rows]
-    _call("moe_expert_linear", status, stream, int(W), int(P), int(K), int(N), _TYPES[dtype], int(act),
-          _typed(x, "x", dtype, [int(n) * K for n in x_rows]), _i64_array(x_rows),
+    _call("moe_expert_linear", status, stream, int(W), int(P), int(K), int(N), _TYPES[dtype],
+          int(act), _typed(x, "x", dtype, [int(n) * K for n in x_rows]), _i64_array(x_rows),
           _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
           _typed(weight, "weight", dtype, [P * NW * K] * W),
           _typed(bias, "bias", dtype, [P * NW] * W), _typed(residual, "residual", dtype, narrow),
@@ -578,8 +585,8 @@ def moe_expert_linear_backward(W, P, K, N, act, x, x_rows, expert_offsets, weigh
     if len(x_rows) != W:
         raise ValueError("x_rows needs W entries")
     wide, xs, ws = [int(n) * NW for n in x_rows], [int(n) * K for n in x_rows], [P * NW * K] * W
-    _call("moe_expert_linear_backward", status, stream, int(W), int(P), int(K), int(N), _TYPES[dtype],
-          int(act), _typed(x, "x", dtype, xs), _i64_array(x_rows),
+    _call("moe_expert_linear_backward", status, stream, int(W), int(P), int(K), int(N),
+          _TYPES[dtype], int(act), _typed(x, "x", dtype, xs), _i64_array(x_rows),
           _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
           _typed(weight, "weight", dtype, ws), _typed(pre, "pre", dtype, wide),
           _typed(d_out, "d_out", dtype, [int(n) * N for n in x_rows]),

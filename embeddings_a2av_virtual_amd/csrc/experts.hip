@@ -1308,7 +1308,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         else hipLaunchKernelGGL(k_expert_dbias<Fp16>, grid, dim3(256), 0, stream, g);
     }
     if (d_x && !launch_product<kDx>(a, type, shape, fast, tiles, stream)) return A2AV_EHIP;
-        if (d_weight) {
+    if (d_weight) {
         // Few rows an expert: the tile's sums are short and its stores long, and
         // four workgroups of the middle size on a compute unit cover the one
         // with the other. (K 7168, NW 4096, bf16: 815 against 887 us at 256 rows

@@ -435,8 +435,19 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
             }
             const bool in = sub < a.groups && before < a.topk_groups;
             kept = (uint32_t)((__ballot(in) >> (L == 64 ? 0 : lane & 48)));
-            if constexpr (!BY_LOGIT) {
-                const float low = -lanes_max<L>(in ? -gs : -inf), high = lanes_max<L>(sub < a.groups && !in ? gs : -inf);
+            const float low = -lanes_max<L>(in ? -gs : -inf);
+            if constexpr (BY_LOGIT) {
+                // Logits that differ may have equal scores in double, which leave
+                // the choice to the group's number: saturated, vanished or tiny
+                // ones. From 2^-20 to 16 (softmax: at most 64 below the largest)
+                // the nearest other logit is 2^-24 of it away or more, and the
+                // scores then differ by over 2^-46 of a score of 1, or of the
+                // score itself: far above the errors of double. Where that holds
+                // for the last group kept, its score is no other logit's.
+                const float size = fabsf(low);
+                unsure = !(low == -inf || (size >= 0x1p-20f && (a.sigmoid ? size <= 16.0f : m - low <= 64.0f)));
+            } else {
+                const float high = lanes_max<L>(sub < a.groups && !in ? gs : -inf);
                 unsure = !(low - high > 4 * key_err + 0x1p-20f * fmaxf(fabsf(low), fabsf(high)));
                 if (high == -inf && low > -inf) unsure = false;
             }
@@ -508,8 +519,7 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
                 head = at < V ? sorted[wave][at][lane] : 0;
             }
         }
-        if constexpr (kIds) unsure = false;
-        else unsure |= !closed;  // more candidates than there is room for
+        unsure |= !closed;  // more candidates than there is room for
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (is_bad || !store) {

@@ -146,6 +146,45 @@ def test_route_masks_infinities_and_nan(sigmoid, groups, E):
     check_route([z], sigmoid, bias, *groups, k, True, 1.0)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("E", [32, 256, 512])
+def test_route_groups_whose_best_scores_are_equal_in_double(E, kind, sigmoid):
+    """Groups by their best expert, whose logits differ where the scores do not:
+    the lowest group is kept, not the one with the larger logit."""
+    g = torch.Generator().manual_seed(14)
+    T, groups = 16, 8
+    per = E // groups
+    z = torch.randn(T, E, generator=g).clamp(-2, 2)
+    best = torch.zeros(T, groups)
+    best[0] = 40.0 + torch.arange(groups)          # sigmoid 1
+    best[1] = 6.0
+    best[2] = torch.tensor([5, 6, 7, 8, 6, 7, 5, 6.0])
+    best[3] = torch.tensor([36, 50, 3, 37, 60, 38, 2, 40.0])
+    z[4] = z[5] = z[6] = -1000.0
+    best[4] = -900.0 + torch.arange(groups)        # sigmoid 0
+    best[5] = -800.0 - 10 * torch.arange(groups)
+    best[5, 6] = 5.0                               # softmax 0 beside it
+    best[6] = -5e-7 * torch.arange(groups)
+    z[7:10] = -3.0
+    best[7] = 1e-7 * torch.arange(groups)          # about 1 / 2
+    best[8] = torch.tensor([0, 6e-8, 0, 1.2e-7, 1e-3, 0, 2e-7, 0])
+    best[9] = torch.tensor([-math.inf, 1, -math.inf, 0, -math.inf, -math.inf, -math.inf, -math.inf])
+    z[9].view(groups, per)[[0, 2, 4, 5, 6, 7]] = -math.inf
+    best[10] = 16.0 + 2.0 ** -6 * torch.arange(groups)
+    best[11] = 30.0 + 2.0 ** -5 * torch.arange(groups)
+    best[12] = 2.5 + 2.0 ** -6 * torch.arange(groups)
+    best[13] = torch.tensor([3, 3, 90, 3, 3, 80, 3, 3.0])
+    best[14] = 700.0 * torch.arange(groups).flip(0)
+    best[15] = 20.0
+    z.view(T, groups, per)[:, :, 1] = best
+    z = z.to(TYPES[kind])
+    for topk_groups in (1, 3, 6):
+        k = min(5, topk_groups * per)
+        check_route([z], sigmoid, None, groups, topk_groups, 1, k, True, 1.0)
+        check_route([z], sigmoid, torch.zeros(E), groups, topk_groups, 2, k, True, 1.0)
+
+
 def test_route_poisoned_status_writes_nothing():
     z = torch.randn(4, 16)
     st, ids, w = gpu_route([z], False, None, 1, 1, 1, 2, True, 1.0, status=64)

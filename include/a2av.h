@@ -517,7 +517,8 @@ int moe_combine_grouped(int W, int64_t T, int k, int E, int64_t H, const int64_t
  * groups (ties: lowest group) keep their experts. The k largest c of those,
  * in descending order, are the ids. c and the group scores are compared as
  * evaluated in double; of equal c the larger logit comes first, then the
- * lowest id. The bias (of a load balancer) only selects:
+ * lowest id (so of groups that equal scores tie, the lowest, whatever their
+ * logits). The bias (of a load balancer) only selects:
  *   weights[j] = scale * s[id_j]                          (renorm 0)
  *   weights[j] = scale * s[id_j] / sum_i s[id_i], or 0 if that sum is 0  (1)
  * (in fp32; a score that double rounds to 0, at about e^-709, is 0)

@@ -32,7 +32,11 @@ enum { kForward, kDx, kDweight };
 struct Bf16 {
     typedef bf16x8 frag;
     static __device__ __forceinline__ float to_float(uint16_t v) { return bf16_lo(v); }
-    static __device__ __forceinline__ uint16_t from_float(float f) { return (uint16_t)to_bf16(f); }
+    // to nearest even by the conversion instruction (NaN stays some NaN): ten
+    // instructions an element less than by integers
+    static __device__ __forceinline__ uint16_t from_float(float f) {
+        return __builtin_bit_cast(uint16_t, (__bf16)f);
+    }
     static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -732,6 +736,8 @@ __global__ __launch_bounds__(WM *WC *kWave, STEP == 32 ? 4 : 2) void k_expert_ti
     static_assert( (STEP == 64 || WM * WC <= 4 * kParts), "");
     const int in = wave / kParts;
     f32x4 *sums = (f32x4 *)(in == 0 ? a0 : in == 1 ? a1 : in == 2 ? a2 : b0) + wave % kParts * (kPart / 16);
+    uint16_t *const out0 = (uint16_t *)a.out[d], *const pre0 = (uint16_t *)a.pre[d];
+    const uint16_t *const bias0 = (const uint16_t *)a.bias[d], *const residual0 = (const uint16_t *)a.residual[d];
 #pragma unroll
     for (int p = 0; p < S::kBlocksM / kPass; p++) {
         if (p * kPass * WM * 32 >= left) break;
@@ -748,35 +754,37 @@ __global__ __launch_bounds__(WM *WC *kWave, STEP == 32 ? 4 : 2) void k_expert_ti
                          ((v * 8 + g * 2 + (lane >> 5)) ^ (lane & 15 & (kCols / 4 - 1)))] = y;
                 }
         asm volatile("" ::: "memory");
-        const int per = glu ? kCols / 16 : kCols / 8;  // lanes a row
-        for (int r = lane / per; r < kPass * 32; r += kWave / per) {
-            const int64_t m = m0 + ((p * kPass + (r >> 5)) * WM + wm) * 32 + (r & 31);
-            const int q = lane % per;
-            if (m >= M) continue;
-            // gated: blocks of 16 gate and 16 up columns alternate
-            const int at = glu ? (q >> 1) * 8 + (q & 1) * 2 : q * 2;
-            const auto take = [&](int i, float(&y)[8]) {
-                const f32x4 lo = sums[r * (kCols / 4) + ((at + i) ^ (r & 15 & (kCols / 4 - 1)))];
-                const f32x4 hi = sums[r * (kCols / 4) + ((at + i + 1) ^ (r & 15 & (kCols / 4 - 1)))];
+        const int64_t c = c0 + wc * kCols;
+        const auto row_of = [&](int r) { return m0 + ((p * kPass + (r >> 5)) * WM + wm) * 32 + (r & 31); };
+        // eight columns of row r of the pass, from the row's chunk `at` on
+        const auto take = [&](int r, int at, float(&y)[8]) {
+            const f32x4 lo = sums[r * (kCols / 4) + (at ^ (r & 15 & (kCols / 4 - 1)))];
+            const f32x4 hi = sums[r * (kCols / 4) + ((at + 1) ^ (r & 15 & (kCols / 4 - 1)))];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    y[c] = lo[c];
-                    y[c + 4] = hi[c];
-                }
-            };
-            float y[8];
-            take(0, y);
-            const int64_t c = c0 + wc * kCols;
-            if constexpr (KIND == kForward) {
+            for (int i = 0; i < 4; i++) {
+                y[i] = lo[i];
+                y[i + 4] = hi[i];
+            }
+        };
+        if constexpr (KIND == kForward) {
+            const int per = glu ? kCols / 16 : kCols / 8;  // lanes a row
+            for (int r = lane / per; r < kPass * 32; r += kWave / per) {
+                const int64_t m = row_of(r);
+                const int q = lane % per;
+                if (m >= M) continue;
+                // gated: blocks of 16 gate and 16 up columns alternate
+                const int at = glu ? (q >> 1) * 8 + (q & 1) * 2 : q * 2;
                 const int64_t n = (glu ? c / 2 : c) + q * 8, row = row0 + m;
                 if (n >= a.N) continue;
-                const uint16_t *bias = (const uint16_t *)a.bias[d] + (int64_t)j * a.NW + n;
-                uint16_t *pre = (uint16_t *)a.pre[d] + row * a.NW + n;
+                float y[8];
+                take(r, at, y);
+                const uint16_t *bias = bias0 + (int64_t)j * a.NW + n;
+                uint16_t *pre = pre0 + row * a.NW + n;
                 if (a.has_bias) add8<T>(y, bias);
                 if (a.has_pre) put8<T>(pre, y);
                 if (glu) {
                     float up[8];
-                    take(4, up);
+                    take(r, at + 4, up);
                     if (a.has_bias) add8<T>(up, bias + a.N);
                     if (a.has_pre) put8<T>(pre + a.N, up);
 #pragma unroll
@@ -785,12 +793,26 @@ __global__ __launch_bounds__(WM *WC *kWave, STEP == 32 ? 4 : 2) void k_expert_ti
 #pragma unroll
                     for (int i = 0; i < 8; i++) y[i] = act_of(a.act, y[i]);
                 }
-                if (a.has_residual) add8<T>(y, (const uint16_t *)a.residual[d] + row * a.N + n);
-                put8<T>((uint16_t *)a.out[d] + row * a.N + n, y);
-            } else {
-                if (c + q * 8 >= C) continue;
-                const int64_t row = KIND == kDx ? row0 + m : (int64_t)j * a.NW + m;
-                put8<T, KIND == kDweight>((uint16_t *)a.out[d] + row * a.K + c + q * 8, y);
+                if (a.has_residual) add8<T>(y, residual0 + row * a.N + n);
+                put8<T>(out0 + row * a.N + n, y);
+            }
+        } else {
+            // several rows' LDS reads in flight
+            constexpr int kPer = kCols / 8, kRows = kWave / kPer, kTimes = kPass * 32 / kRows;
+            constexpr int kBatch = kTimes < 4 ? kTimes : 4;
+            const int q = lane % kPer;
+            const bool in_c = c + q * 8 < C;
+            uint16_t *const at = out0 + (KIND == kDx ? row0 : (int64_t)j * a.NW) * a.K + c + q * 8;
+#pragma unroll
+            for (int r0 = 0; r0 < kPass * 32; r0 += kBatch * kRows) {
+                float y[kBatch][8];
+#pragma unroll
+                for (int i = 0; i < kBatch; i++) take(r0 + i * kRows + lane / kPer, q * 2, y[i]);
+#pragma unroll
+                for (int i = 0; i < kBatch; i++) {
+                    const int64_t m = row_of(r0 + i * kRows + lane / kPer);
+                    if (m < M && in_c) put8<T, KIND == kDweight>(at + m * a.K, y[i]);
+                }
             }
         }
         asm volatile("" ::: "memory");

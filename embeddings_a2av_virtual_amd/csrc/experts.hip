@@ -1333,11 +1333,12 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
     if (d_weight) {
         // Few rows an expert: the tile's sums are short and its stores long, and
         // four workgroups of the middle size on a compute unit cover the one
-        // with the other. (K 7168, NW 4096, bf16: 815 against 887 us at 256 rows
-        // an expert, 1215 against 1206 at 512, 993 against 954 at 1024; tiles of
-        // 256 x 128, with three quarters of the L2's reads, 950 against 960 us.)
+        // with the other. (K 7168, bf16: 186 against 222 us at 64 rows an expert
+        // and NW 2048; with NW 4096 758 against 769 at 256, 1173 against 1115 at
+        // 512, 985 against 921 at 1024. Tiles of 256 x 128, with three quarters
+        // of the L2's reads, take as long as the middle size.)
         int s = fast ? shape_of(R, n, a.NW, K) : kSmall;
-        if (s == kBig && R < 512 * n) s = kMid;
+        if (s == kBig && R < 384 * n) s = kMid;
         if (!launch_product<kDweight>(b, type, s, fast, 0, stream)) return A2AV_EHIP;
     }
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;

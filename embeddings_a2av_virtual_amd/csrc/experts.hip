@@ -1220,6 +1220,10 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
         if (!weight[d] || (bias && !bias[d])) return A2AV_EARG;
         if (x_rows[d] > 0 && (!x[d] || !out[d] || (residual && !residual[d]) || (pre && !pre[d])))
             return A2AV_EARG;
+        // other tiles still read x; pre is written before the residual is read
+        if (x_rows[d] > 0 && (out[d] == x[d] || (pre && (pre[d] == x[d] || pre[d] == out[d]))))
+            return A2AV_EARG;
+        if (x_rows[d] > 0 && pre && residual && pre[d] == residual[d]) return A2AV_EARG;
         a.a[d] = x[d];
         a.b[d] = weight[d];
         a.bias[d] = bias ? bias[d] : nullptr;
@@ -1299,6 +1303,9 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         if (!weight[d] || (d_weight && !d_weight[d]) || (d_bias && !d_bias[d])) return A2AV_EARG;
         if (x_rows[d] > 0 && (!x[d] || !d_out[d] || (!none && (!pre[d] || !d_pre[d])) || (d_x && !d_x[d])))
             return A2AV_EARG;
+        // other tiles still read d_pre, and d_weight x
+        if (x_rows[d] > 0 && d_x && (d_x[d] == x[d] || d_x[d] == (none ? d_out[d] : d_pre[d]))) return A2AV_EARG;
+        if (x_rows[d] > 0 && !none && d_pre[d] == x[d]) return A2AV_EARG;
         g.pre[d] = none ? nullptr : pre[d];
         g.d_out[d] = d_out[d];
         g.d_pre[d] = none ? nullptr : d_pre[d];

@@ -665,7 +665,9 @@ size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int
  * Two kernels: a plan that checks the offsets and lists the row tiles of all
  * experts, and the products on matrix cores. Sizes and alignments of any kind
  * are accepted; rows that are 16-byte multiples at 16-byte-aligned bases take
- * the fast path.
+ * the fast path. Arrays that are written overlap no others but, as said, the
+ * residual (out or pre at the base of x, or pre at that of out or the
+ * residual: A2AV_EARG).
  */
 int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int act,
                       const void *const *x, const int64_t *x_rows,
@@ -698,7 +700,9 @@ size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64
  *   d_bias         host array of W device [P][NW], or NULL: not wanted
  *   workspace      device scratch of >= ..._backward_workspace_bytes()
  *   status         as moe_expert_linear
- * Rows past a rank's total are not read, and untouched in d_pre and d_x.
+ * Rows past a rank's total are not read, and untouched in d_pre and d_x. d_pre
+ * may be pre; otherwise arrays that are written overlap no others (d_x at the
+ * base of x or of d_pre, or d_pre at that of x: A2AV_EARG).
  * One kernel each for the plan, d_pre (with the bias sums of row blocks), the
  * bias, d_x and d_weight, less what is not wanted.
  */

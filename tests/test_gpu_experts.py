@@ -72,7 +72,7 @@ class Experts:
         assert all(b.guards_intact() for b in ob + pb)
         return int(st.item()), [x.cpu() for x in out], [x.cpu() for x in pre]
 
-    def backward(self, offsets=None, want=("d_x", "d_weight", "d_bias"), status=0):
+    def backward(self, offsets=None, want=("d_x", "d_weight", "d_bias"), status=0, in_place=False):
         rows = [n + self.spare for n in self.tot]
         none = self.act == "none"
         bufs = {"d_pre": [(n + self.spare, self.NW) for n in self.tot], "d_x": [x.shape for x in self.x],
@@ -81,11 +81,14 @@ class Experts:
         arg = {k: [v for _, v in x] for k, x in made.items()}
         st = torch.full((1,), status, dtype=torch.int32, device="cuda")
         act = ACTS[self.act]
+        h = None if none else self._dev(self.h)
+        if in_place:
+            arg["d_pre"] = h
         ws = torch.empty(B.moe_expert_linear_backward_workspace_bytes(self.W, self.P, self.K, self.N, act, rows),
                          dtype=torch.uint8, device="cuda").random_()
         B.moe_expert_linear_backward(self.W, self.P, self.K, self.N, act, self._dev(self.x), rows,
                                      (self.offsets if offsets is None else offsets).cuda(), self._dev(self.weight),
-                                     None if none else self._dev(self.h), self._dev(self.d_out),
+                                     h, self._dev(self.d_out),
                                      None if none else arg["d_pre"],
                                      *[arg[k] if k in want else None for k in ("d_x", "d_weight", "d_bias")], ws, st)
         torch.cuda.synchronize()
@@ -251,6 +254,21 @@ def test_bases_of_other_alignments(pad):
 
 def test_residual_in_place():
     Experts([[20, 70]], 64, 48, "bf16", "gelu", 7).check_forward(in_place=True)
+
+
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+@pytest.mark.parametrize("K,N", [(64, 48), (33, 31)])
+def test_gradient_of_pre_in_place(K, N, act):
+    e = Experts([[20, 70, 0, 150]], K, N, "bf16", act, 8)
+    st, apart = e.backward()
+    st2, there = e.backward(in_place=True)
+    assert st == st2 == 0
+    n = e.tot[0]
+    for k in apart:
+        a, b = apart[k][0], there[k][0]
+        if k in ("d_pre", "d_x"):
+            a, b = a[:n], b[:n]
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)), k
 
 
 @pytest.mark.parametrize("K,N", [(64, 64), (72, 40), (33, 31), (1024, 512), (4096, 24)])

@@ -93,7 +93,7 @@ def test_combine_return_backward(L):
 
 
 def test_expert_linear(L):
-    p, r = _ptrs(16, 16), _rows(20, 0)
+    p, q, s, r = _ptrs(16, 16), _ptrs(32, 32), _ptrs(48, 48), _rows(20, 0)
     need = L.moe_expert_linear_workspace_bytes(2, 4, 64, 32, 0, r)
     assert need > 0
     for bad in ((0, 4, 64, 32, 0, r), (2, 0, 64, 32, 0, r), (2, 2049, 64, 32, 0, r), (2, 4, 0, 32, 0, r),
@@ -103,23 +103,24 @@ def test_expert_linear(L):
         assert L.moe_expert_linear_workspace_bytes(*bad) == 0
         assert L.moe_expert_linear_backward_workspace_bytes(*bad) == 0
 
-    def call(type=1, act=0, x=p, rows=r, off=vp(16), w=p, bias=None, res=None, out=p, pre=None, ws=vp(256), n=need,
+    def call(type=1, act=0, x=p, rows=r, off=vp(16), w=p, bias=None, res=None, out=q, pre=None, ws=vp(256), n=need,
              st=vp(16)):
         return L.moe_expert_linear(2, 4, 64, 32, type, act, x, rows, off, w, bias, res, out, pre, ws, n, st, None)
 
     half = _ptrs(None, 16)
     for kw in (dict(type=0), dict(type=3), dict(act=5), dict(x=None), dict(rows=None), dict(off=None), dict(w=None),
                dict(out=None), dict(ws=None), dict(ws=vp(260)), dict(n=need - 1), dict(st=None), dict(x=half),
-               dict(w=_ptrs(16, None)), dict(bias=half), dict(res=half), dict(out=half), dict(pre=half)):
+               dict(w=_ptrs(16, None)), dict(bias=half), dict(res=half), dict(out=half), dict(pre=half),
+               dict(out=p), dict(pre=p), dict(pre=q), dict(pre=s, res=s)):
         assert call(**kw) == EARG, kw
 
 
 def test_expert_linear_backward(L):
-    p, r = _ptrs(16, 16), _rows(20, 0)
+    p, q, s, r = _ptrs(16, 16), _ptrs(32, 32), _ptrs(48, 48), _rows(20, 0)
     need = L.moe_expert_linear_backward_workspace_bytes(2, 4, 64, 32, 3, r)
     assert need > L.moe_expert_linear_workspace_bytes(2, 4, 64, 32, 3, r)
 
-    def call(type=1, act=3, x=p, off=vp(16), w=p, pre=p, g=p, dpre=p, dx=p, dw=p, db=p, ws=vp(256), n=need, st=vp(16)):
+    def call(type=1, act=3, x=p, off=vp(16), w=p, pre=p, g=p, dpre=q, dx=s, dw=p, db=p, ws=vp(256), n=need, st=vp(16)):
         return L.moe_expert_linear_backward(2, 4, 64, 32, type, act, x, r, off, w, pre, g, dpre, dx, dw, db, ws, n,
                                             st, None)
 
@@ -127,5 +128,6 @@ def test_expert_linear_backward(L):
     for kw in (dict(type=0), dict(act=9), dict(x=None), dict(off=None), dict(w=None), dict(pre=None), dict(g=None),
                dict(dpre=None), dict(act=0), dict(act=0, pre=None), dict(act=0, dpre=None), dict(ws=None),
                dict(n=need - 1), dict(st=None), dict(x=half), dict(pre=half), dict(g=half), dict(dpre=half),
-               dict(dx=half), dict(dw=half), dict(db=half)):
+               dict(dx=half), dict(dw=half), dict(db=half), dict(dx=p), dict(dx=q), dict(dpre=p),
+               dict(act=0, pre=None, dpre=None, g=s)):
         assert call(**kw) == EARG, kw

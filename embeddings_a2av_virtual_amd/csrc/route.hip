@@ -438,7 +438,6 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
             }
             const bool in = sub < a.groups && before < a.topk_groups;
             kept = (uint32_t)((__ballot(in) >> (L == 64 ? 0 : lane & 48)));
-            const float low = -lanes_max<L>(in ? -gs : -inf);
             if constexpr (BY_LOGIT) {
                 // Logits that differ may have equal scores in double, which leave
                 // the choice to the group's number: saturated, vanished or tiny
@@ -447,12 +446,21 @@ __global__ __launch_bounds__(256) void k_moe_route(const RouteArgs a, bool vec, 
                 // scores then differ by over 2^-46 of a score of 1, or of the
                 // score itself: far above the errors of double. Where that holds
                 // for the last group kept, its score is no other logit's.
+                const float low = -lanes_max<L>(in ? -gs : -inf);
                 const float size = fabsf(low);
                 unsure = !(low == -inf || (size >= 0x1p-20f && (a.sigmoid ? size <= 16.0f : m - low <= 64.0f)));
             } else {
-                const float high = lanes_max<L>(sub < a.groups && !in ? gs : -inf);
-                unsure = !(low - high > 4 * key_err + 0x1p-20f * fmaxf(fabsf(low), fabsf(high)));
-                if (high == -inf && low > -inf) unsure = false;
+                // The least that a kept group's exact score can be, against the
+                // most of a dropped one. A key is off by key_err and half a step
+                // of itself (the bias's sum), however small the two keys' sum is;
+                // twice that and more for the sum's own rounding and those here.
+                // Infinite scores are what they are; beyond fp32's range a
+                // dropped one is above every kept one.
+                const float off = 2 * key_err + 0x1p-22f * (fabsf(t1) + (a.group_top == 1 ? 0.0f : fabsf(t2)));
+                const bool exact = fabsf(gs) == inf;
+                const float low = -lanes_max<L>(in ? (exact ? -gs : off - gs) : -inf);
+                const float high = lanes_max<L>(sub < a.groups && !in ? (exact ? gs : gs + off) : -inf);
+                unsure = !(low > high);
             }
         }
         uint32_t s[V];

@@ -682,14 +682,16 @@ __global__ __launch_bounds__(256) void k_moe_route_backward_any(const RouteGradA
         if (a.sigmoid && on) v *= 1.0f / (1.0f + expf(logit_at<TYPE>(row, id)));
         float m = 0.0f, f = 0.0f;
         const bool full = !a.sigmoid && !a.renorm;
+        const auto part = [&](float z) { return z == -inf ? 0.0f : expf(z - m); };
         if (full) {
             m = -inf;
             for (int e = lane; e < a.E; e += kWave) m = fmaxf(m, logit_at<TYPE>(row, e));
             m = wave_max(m);
             float sum = 0.0f;
-            for (int e = lane; e < a.E; e += kWave) sum += m == -inf ? 0.0f : expf(logit_at<TYPE>(row, e) - m);
+            // a row of -inf has no gradient; NaN passes on
+            for (int e = lane; e < a.E; e += kWave) sum += part(logit_at<TYPE>(row, e));
             sum = wave_sum(sum);
-            f = sum > 0 ? dot / sum : 0.0f;
+            f = sum == 0.0f ? 0.0f : dot / sum;
         }
         for (int e0 = 0; e0 < a.E; e0 += kWave) {
             const int e = e0 + lane;
@@ -700,7 +702,7 @@ __global__ __launch_bounds__(256) void k_moe_route_backward_any(const RouteGradA
                 d += ej == e ? vj : 0.0f;
             }
             if (e < a.E) {
-                if (full && m != -inf) d -= f * expf(logit_at<TYPE>(row, e) - m);
+                if (full) d -= f * part(logit_at<TYPE>(row, e));
                 store_logit<TYPE>(out, e, d);
             }
         }

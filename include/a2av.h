@@ -559,7 +559,7 @@ int moe_route(int W, int64_t T, int k, int E, int type, int score,
  *   status         A2AV_ST_BAD_EXPERT for an id outside [0, E): nothing is
  *                  written.
  * Ids may repeat (their gradients add up). A token with NaN weights gets NaN
- * for its chosen experts.
+ * for its chosen experts, and with softmax and renorm 0 for all of them.
  * Two kernels: a range check of the ids, then the gradient.
  */
 int moe_route_backward(int W, int64_t T, int k, int E, int type, int score,

@@ -1306,6 +1306,8 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         // other tiles still read d_pre, and d_weight x
         if (x_rows[d] > 0 && d_x && (d_x[d] == x[d] || d_x[d] == (none ? d_out[d] : d_pre[d]))) return A2AV_EARG;
         if (x_rows[d] > 0 && !none && d_pre[d] == x[d]) return A2AV_EARG;
+        // d_pre's rows are wider than those of d_out that are still to be read
+        if (x_rows[d] > 0 && act == A2AV_ACT_SWIGLU && d_pre[d] == d_out[d]) return A2AV_EARG;
         g.pre[d] = none ? nullptr : pre[d];
         g.d_out[d] = d_out[d];
         g.d_pre[d] = none ? nullptr : d_pre[d];

@@ -702,7 +702,8 @@ size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64
  *   status         as moe_expert_linear
  * Rows past a rank's total are not read, and untouched in d_pre and d_x. d_pre
  * may be pre; otherwise arrays that are written overlap no others (d_x at the
- * base of x or of d_pre, or d_pre at that of x: A2AV_EARG).
+ * base of x or of d_pre, d_pre at that of x or, with A2AV_ACT_SWIGLU, of
+ * d_out: A2AV_EARG).
  * One kernel each for the plan, d_pre (with the bias sums of row blocks), the
  * bias, d_x and d_weight, less what is not wanted.
  */

@@ -1,0 +1,42 @@
+"""Arrays that a call writes while others still read them are refused at the C
+ABI, before any HIP call is made (no GPU needed). Every array has a base of its
+own but the two in question."""
+import ctypes
+
+import pytest
+
+EARG = -1
+vp = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def L():
+    from embeddings_a2av_virtual_amd import _binding
+    return _binding.lib()
+
+
+def _ptrs(*v):
+    return (ctypes.c_void_p * len(v))(*v)
+
+
+def _rows(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def test_gated_gradient_over_d_out(L):
+    """SwiGLU's d_pre has rows twice as wide as d_out's: row r lands on rows
+    that other workgroups have not read."""
+    bases = {n: _ptrs(1 << 20 | i << 12, 1 << 21 | i << 12) for i, n in
+             enumerate(("x", "w", "pre", "d_out", "d_pre", "d_x", "d_w", "d_b"))}
+    r = _rows(20, 7)
+    need = L.moe_expert_linear_backward_workspace_bytes(2, 4, 64, 32, 4, r)
+
+    def call(**kw):
+        b = dict(bases, **kw)
+        return L.moe_expert_linear_backward(2, 4, 64, 32, 1, 4, b["x"], r, vp(1 << 22), b["w"], b["pre"], b["d_out"],
+                                            b["d_pre"], b["d_x"], b["d_w"], b["d_b"], vp(1 << 23), need, vp(1 << 24),
+                                            None)
+
+    assert call(d_pre=bases["d_out"]) == EARG
+    assert call(d_pre=_ptrs(bases["d_pre"][0], bases["d_out"][1])) == EARG
+    assert call(d_pre=bases["x"]) == EARG and call(d_x=bases["d_pre"]) == EARG

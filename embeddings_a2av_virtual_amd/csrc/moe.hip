@@ -1377,6 +1377,15 @@ A2AV_API int moe_combine(int W, int64_t T, int k, int64_t H, const void *const *
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }
 
+// A rank's gradient rows begin where a rank's d_out does, which other waves and
+// workgroups still read; rows[d]: rows that d_rows[d] has.
+static bool over_d_out(int W, void *const *d_rows, const int64_t *rows, const void *const *d_out) {
+    for (int d = 0; d < W; d++)
+        for (int s = 0; s < W; s++)
+            if ((!rows || rows[d] > 0) && d_rows[d] == d_out[s]) return true;
+    return false;
+}
+
 A2AV_API size_t moe_combine_backward_workspace_bytes(int W, int64_t T, int k) {
     if (W < 1 || W > A2AV_MAX_W || T < 0 || k < 1) return 0;
     if (T > ((int64_t)1 << 31) / k || T * k >= ((int64_t)1 << 31)) return 0;
@@ -1411,6 +1420,7 @@ A2AV_API int moe_combine_backward(int W, int64_t T, int k, int64_t H, const void
         aligned = aligned && ((uintptr_t)back[r] % 16 == 0) && ((uintptr_t)d_out[r] % 16 == 0) &&
                   ((uintptr_t)d_back[r] % 16 == 0);
     }
+    if (T > 0 && over_d_out(W, d_back, nullptr, d_out)) return A2AV_EARG;
     a.mark = (int32_t *)workspace;
     a.status = status;
     a.T = T;
@@ -1474,6 +1484,7 @@ A2AV_API int moe_combine_return_backward(int W, int64_t T, int k, int E, int64_t
         aligned = aligned && ((uintptr_t)recv[r] % 16 == 0) && ((uintptr_t)d_out[r] % 16 == 0) &&
                   ((uintptr_t)d_recv[r] % 16 == 0);
     }
+    if (T > 0 && over_d_out(W, d_recv, recv_rows, d_out)) return A2AV_EARG;
     unsigned char *ws = (unsigned char *)workspace;
     const size_t table = round256((size_t)W * (size_t)E * 8);
     const size_t plan = moe_combine_return_workspace_bytes(W, T, k, E);

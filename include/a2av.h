@@ -588,6 +588,8 @@ size_t moe_combine_backward_workspace_bytes(int W, int64_t T, int k);
  *   status        A2AV_ST_BAD_PERM if a perm entry is outside [0, T*k) or
  *                 appears twice (two slots would write one row): nothing but
  *                 the workspace is written.
+ * d_back may be back; otherwise arrays that are written overlap no others (a
+ * d_back at the base of a d_out: A2AV_EARG).
  * Three kernels: every slot marks its row, every slot checks its mark, then
  * the gradient (one workgroup per token, its waves taking the slots in turn).
  */
@@ -617,6 +619,8 @@ size_t moe_combine_return_backward_workspace_bytes(int W, int64_t T, int k, int 
  *   status        as moe_unpack_return, and A2AV_ST_BAD_PERM for a perm entry
  *                 that appears twice; nothing but the workspace is written on
  *                 failure.
+ * d_recv may be recv; otherwise arrays that are written overlap no others (a
+ * d_recv at the base of a d_out: A2AV_EARG).
  * The gradient of the tokens behind moe_pack_dispatch is the sum of their
  * slots' rows: moe_combine_return over the rows' gradients with weights of 1.
  * Four kernels: the plan of moe_pack_dispatch, a check of every slot that

@@ -1134,43 +1134,56 @@ static dim3 tile_grid(int64_t columns, int64_t tiles) {
     return dim3((unsigned)columns, (unsigned)y, (unsigned)((tiles + y - 1) / y));
 }
 
-// False for more workgroups than a launch can have.
+// Columns of a product, and column tiles of a shape.
+template <int KIND>
+static int64_t columns_of(const ExpertArgs &a) {
+    return KIND != kForward ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
+}
+template <int KIND>
+static int64_t column_tiles(const ExpertArgs &a, int shape) {
+    if (shape == kFew) return (a.N + 15) / 16;
+    return (columns_of<KIND>(a) + kTile[shape] - 1) / kTile[shape];
+}
+
+// The shape's workgroups fit one launch of the tile kernels (k_expert_any has a
+// grid of three dimensions and takes any number).
+template <int KIND>
+static bool launches(const ExpertArgs &a, int shape, int64_t tiles) {
+    if (KIND == kDweight) tiles = (int64_t)a.W * a.P * ((a.NW + kTile[shape] - 1) / kTile[shape]);
+    return tiles * column_tiles<KIND>(a, shape) <= kMostGroups;
+}
+
 template <int KIND, typename T>
-static bool launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, hipStream_t stream) {
-    const int64_t cols = KIND != kForward ? a.K : a.act == A2AV_ACT_SWIGLU ? (a.N + 15) / 16 * 32 : a.N;
+static void launch_product(ExpertArgs &a, int shape, bool fast, int64_t tiles, hipStream_t stream) {
     const int64_t t = fast ? kTile[shape] : kAny;
-    a.cols = (int)((cols + t - 1) / t);
+    a.cols = (int)(fast ? column_tiles<KIND>(a, shape) : (columns_of<KIND>(a) + kAny - 1) / kAny);
     a.row_tiles = (int)((a.NW + t - 1) / t);
     if (!fast) {
         const dim3 g = KIND == kDweight ? dim3(a.cols, a.row_tiles, a.W * a.P) : tile_grid(a.cols, tiles);
         hipLaunchKernelGGL((k_expert_any<KIND, T>), g, dim3(256), 0, stream, a);
-        return true;
+        return;
     }
     if constexpr (KIND == kForward) {
         if (shape == kFew) {
-            a.cols = (int)((a.N + 15) / 16);
-            if (tiles * a.cols > kMostGroups) return false;
             const dim3 g((unsigned)(tiles * a.cols));
             if (a.act == A2AV_ACT_SWIGLU) hipLaunchKernelGGL((k_expert_few<T, true>), g, dim3(256), 0, stream, a);
             else hipLaunchKernelGGL((k_expert_few<T, false>), g, dim3(256), 0, stream, a);
-            return true;
+            return;
         }
     }
     if (KIND == kDweight) tiles = (int64_t)a.W * a.P * a.row_tiles;
-    if (tiles * a.cols > kMostGroups) return false;
     const dim3 g((unsigned)((tiles * a.cols + 7) / 8 * 8));
     if (shape == kBig) hipLaunchKernelGGL((k_expert_tile<KIND, T, 256, 256, 2, 4, 64>), g, dim3(512), 0, stream, a);
     else if (shape == kMid)
         hipLaunchKernelGGL((k_expert_tile<KIND, T, 128, 128, 2, 2, KIND == kDweight ? 32 : 64>), g, dim3(256), 0, stream, a);
     else
         hipLaunchKernelGGL((k_expert_tile<KIND, T, 64, 64, 2, 2, 64>), g, dim3(256), 0, stream, a);
-    return true;
 }
 
 template <int KIND>
-static bool launch_product(ExpertArgs &a, int type, int shape, bool fast, int64_t tiles, hipStream_t stream) {
-    if (type == A2AV_DT_BF16) return launch_product<KIND, Bf16>(a, shape, fast, tiles, stream);
-    return launch_product<KIND, Fp16>(a, shape, fast, tiles, stream);
+static void launch_product(ExpertArgs &a, int type, int shape, bool fast, int64_t tiles, hipStream_t stream) {
+    if (type == A2AV_DT_BF16) launch_product<KIND, Bf16>(a, shape, fast, tiles, stream);
+    else launch_product<KIND, Fp16>(a, shape, fast, tiles, stream);
 }
 
 // Most tiles of `rows` rows that a product's row tiles can be.
@@ -1248,10 +1261,13 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     // on 8 of 32 experts, K 7168, N 2048, bf16: 72 against 107 us; no gate,
     // 8 experts: 44 against 58 us at K 7168, 55.5 against 55 at K 4096, 58
     // against 44 at K 2048; 12 rows an expert at K 7168: 210 against 172 us.)
-    const int shape = !fast ? kSmall : R <= 4 * n && K >= 4096 ? kFew : shape_of(R, n, 0, a.NW);
+    int shape = R <= 4 * n && K >= 4096 ? kFew : shape_of(R, n, 0, a.NW);
+    const auto tiles = [&] { return most_tiles(x_rows, W, P, kTile[shape]); };
+    if (shape == kFew && !launches<kForward>(a, shape, tiles())) shape = shape_of(R, n, 0, a.NW);
+    fast = fast && launches<kForward>(a, shape, tiles());
+    if (!fast) shape = kSmall;
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], (unsigned char *)workspace, l, status, stream);
-    if (!launch_product<kForward>(a, type, shape, fast, most_tiles(x_rows, W, P, kTile[shape]), stream))
-        return A2AV_EHIP;
+    launch_product<kForward>(a, type, shape, fast, tiles(), stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }
 
@@ -1322,7 +1338,9 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
                aligned16(b.out[d]);
     }
     const int64_t n = (int64_t)W * P;
-    const int shape = fast ? shape_of(R, n, 0, K) : kSmall;
+    int shape = shape_of(R, n, 0, K);
+    const bool fast_x = fast && launches<kDx>(a, shape, most_tiles(x_rows, W, P, kTile[shape]));
+    if (!fast_x) shape = kSmall;
     const int64_t tiles = most_tiles(x_rows, W, P, kTile[shape]);
     g.blocks = kTile[shape] / kBlockRows;
     launch_plan(W, P, x_rows, expert_offsets, kTile[shape], ws, l, status, stream);
@@ -1338,7 +1356,7 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         if (type == A2AV_DT_BF16) hipLaunchKernelGGL(k_expert_dbias<Bf16>, grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL(k_expert_dbias<Fp16>, grid, dim3(256), 0, stream, g);
     }
-    if (d_x && !launch_product<kDx>(a, type, shape, fast, tiles, stream)) return A2AV_EHIP;
+    if (d_x) launch_product<kDx>(a, type, shape, fast_x, tiles, stream);
     if (d_weight) {
         // Few rows an expert: the tile's sums are short and its stores long, and
         // four workgroups of the middle size on a compute unit cover the one
@@ -1346,9 +1364,9 @@ A2AV_API int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int 
         // and NW 2048; with NW 4096 758 against 769 at 256, 1173 against 1115 at
         // 512, 985 against 921 at 1024. Tiles of 256 x 128, with three quarters
         // of the L2's reads, take as long as the middle size.)
-        int s = fast ? shape_of(R, n, a.NW, K) : kSmall;
-        if (s == kBig && R < 384 * n) s = kMid;
-        if (!launch_product<kDweight>(b, type, s, fast, 0, stream)) return A2AV_EHIP;
+        int s = shape_of(R, n, a.NW, K);
+        if (s == kBig && R < 384 * n && launches<kDweight>(b, kMid, 0)) s = kMid;
+        launch_product<kDweight>(b, type, s, fast && launches<kDweight>(b, s, 0), 0, stream);
     }
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

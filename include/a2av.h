@@ -669,7 +669,7 @@ size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int
  * Two kernels: a plan that checks the offsets and lists the row tiles of all
  * experts, and the products on matrix cores. Sizes and alignments of any kind
  * are accepted; rows that are 16-byte multiples at 16-byte-aligned bases take
- * the fast path. Arrays that are written overlap no others but, as said, the
+ * the fast path, up to 2^22 tiles of a product (counted for x_rows). Arrays that are written overlap no others but, as said, the
  * residual (out or pre at the base of x, or pre at that of out or the
  * residual: A2AV_EARG).
  */

@@ -9,7 +9,7 @@
 //
 //   k_expert_plan   checks the offsets, lists the row tiles of all experts
 //   k_expert_tile   one tile of one product, 16-byte rows
-//   k_expert_few    16 columns of up to 16 rows, the weights read once
+//   k_expert_few    16 columns of up to 16 rows, which read their weights once
 //   k_expert_any    one 64 x 64 tile of one product, any size and alignment
 //   k_expert_dpre   d_pre = d_out * act'(pre), with the bias sums of row blocks
 //   k_expert_dbias  the bias sums of an expert's row blocks, in order
@@ -220,6 +220,9 @@ constexpr int kAnyPad = 40;    // LDS row, in elements
 // One 64 x 64 tile by four waves of 32 x 32, elements loaded one by one with
 // their bounds checked; what lies outside is 0 in both operands, so it adds
 // nothing even where the other holds infinities or NaN.
+// Bound by those loads: 16384 rows, K 7168, NW 4096 at a base that is no 16-byte
+// multiple 13.0 / 17.3 / 15.4 ms (forward / d_x / d_weight; 1.0 / 1.0 / 1.2 ms by
+// 16-byte rows).
 template <int KIND, typename T>
 __global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
     __shared__ __align__(16) uint16_t sa[kAny * kAnyPad], sb[kAny * kAnyPad];
@@ -344,30 +347,40 @@ __global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
 
 // ------------------------------------------------------------------ the fast products
 // Tiles of BM rows and BC columns, a contraction step of 64 (whole 128-byte
-// lines), both operands through LDS in two stages that buffer loads fill
-// directly. An operand comes in one of two forms, by what its memory holds
-// contiguously:
+// lines), both operands through LDS stages that buffer loads fill directly
+// (three of the rows' operand, two of the other). An operand comes in one of
+// two forms, by what its memory holds contiguously:
 //   along the contraction (x and weight forward, d_pre for d_x): LDS rows of
 //     64 elements, the eight 16-byte chunks of row r permuted by r % 8, read
 //     as 16-byte fragments;
 //   along the tile's rows or columns (the others): LDS rows are contraction
 //     steps of BM or BC elements, 32-byte units permuted by the row, read with
 //     the transposing LDS load (4 contraction steps x 16 columns a group).
-// Both permutations put the lanes of one LDS access in different banks.
+// The second permutation puts the lanes of one LDS access in different banks;
+// with the first, conflicts are counted for half of the forward product's LDS
+// cycles and a third of d_x's.
 // Rows, columns and contraction steps outside are loaded out of the buffer's
 // range, which writes zeros to LDS; so the last steps can go on loading what
 // nobody reads, and every step waits for the same number of loads.
 //
-// What bounds it, at 16384 rows, K 7168 and 4096 columns in bf16 (one library
-// product of that size: 615-650 us): the matrix cores' power. The kernel needs
-// 1.16 M cycles of each compute unit and its clock falls to 1.5 GHz (767 us;
-// the library's product 1.05 M cycles at 1.6 GHz). Other shapes, same box, all
-// three products (forward / d_x / d_weight, us through): eight waves and two
-// stages of 64 with one barrier a step 848 / 849 / spills; two groups of waves
-// in turn at reading and multiplying 928 / 778 / 852; four stages of 32, whose
-// 64-byte requests double the L2's work, 920 / 834 / 755; four waves of 128 x
-// 128, half the LDS reads but no second wave to issue beside a stalled one,
-// 889 / 818 / 825; this one 875 / 811 / 808 and the fastest on ragged experts.
+// What bounds it, K 7168 and 4096 columns in bf16 (one library product of 16384
+// rows: 615-650 us). 32 equal experts of 512 rows: 806-820 us, 1.2 PFLOP/s, the
+// matrix cores' power (the clock falls to 1.5 GHz). Ragged ones (lognormal):
+// 990-1020 us, and 585-640 against 490-580 at 256 rows an expert: a last row
+// tile of a few rows still loads all of its columns' weights, step by step, and
+// so takes most of a full tile's time; with 256 workgroups at once the calls
+// take as many rounds as the fullest compute unit has tiles. There the matrix
+// cores are busy 60 % of the cycles, and 3.6 GB are read, weights once 1.9 GB.
+// d_x of 256 rows an expert: 3.5 rounds of tiles run as 4, 50 % busy; d_weight
+// on the middle tiles 33 % (eight steps of sums, then 64 KiB of them through
+// LDS and 1.9 GB of stores).
+//
+// Other shapes at 16384 rows, same box, all three products (forward / d_x /
+// d_weight, us through): eight waves and two stages of 64 with one barrier a step 848 / 849 / spills; two groups of waves in turn at reading and
+// multiplying 928 / 778 / 852; four stages of 32, whose 64-byte requests double
+// the L2's work, 920 / 834 / 755; four waves of 128 x 128, half the LDS reads
+// but no second wave to issue beside a stalled one, 889 / 818 / 825; this one
+// 875 / 811 / 808.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef __attribute__((address_space(3))) void lds_void;
@@ -443,8 +456,8 @@ struct Operand {
     // The memory row of a step that load i of a wave begins with: the row bits
     // that unit_shift goes by (0, 1 and 3) come from the wave and the lane.
     static __device__ __forceinline__ int first(int i, int wave) {
-        if constexpr (kPer == 32 && kWaves == 4) return (wave & 1) << 1 | (wave >> 1) << 3 | (i & 1) << 2 | (i >> 1) << 4;
-        else if constexpr (kPer == 32) return (wave & 1) << 1 | (wave >> 1) << 3 | (i & 1) << 2 | (i >> 1) << 5;
+        static_assert(kWaves == (kPer == 32 ? 8 : 4), "");
+        if constexpr (kPer == 32) return (wave & 1) << 1 | (wave >> 1) << 3 | (i & 1) << 2 | (i >> 1) << 5;
         else if constexpr (kPer == 16) return wave << 3 | (i & 1) << 2 | (i >> 1) << 5;
         else return wave << 3 | i << 5;
     }
@@ -1261,6 +1274,10 @@ A2AV_API int moe_expert_linear(int W, int P, int64_t K, int64_t N, int type, int
     // on 8 of 32 experts, K 7168, N 2048, bf16: 72 against 107 us; no gate,
     // 8 experts: 44 against 58 us at K 7168, 55.5 against 55 at K 4096, 58
     // against 44 at K 2048; 12 rows an expert at K 7168: 210 against 172 us.)
+    // The rows are those that x_rows allows. All of them on one expert: its
+    // weights are read once for every 16 rows, from the L2 then (128 rows of 32
+    // experts, NW 4096: 82 us against 119 of one row more by tiles; 1024 of 256,
+    // NW 1024: 155 against 121).
     int shape = R <= 4 * n && K >= 4096 ? kFew : shape_of(R, n, 0, a.NW);
     const auto tiles = [&] { return most_tiles(x_rows, W, P, kTile[shape]); };
     if (shape == kFew && !launches<kForward>(a, shape, tiles())) shape = shape_of(R, n, 0, a.NW);

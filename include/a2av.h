@@ -667,7 +667,8 @@ size_t moe_expert_linear_workspace_bytes(int W, int P, int64_t K, int64_t N, int
  *                   descend), A2AV_ST_SEND_OVERRUN (a total above x_rows):
  *                   nothing but the workspace is written.
  * Two kernels: a plan that checks the offsets and lists the row tiles of all
- * experts, and the products on matrix cores. Sizes and alignments of any kind
+ * experts, and the products on matrix cores; their tiles are chosen for as many
+ * rows as x_rows allows. Sizes and alignments of any kind
  * are accepted; rows that are 16-byte multiples at 16-byte-aligned bases take
  * the fast path, up to 2^22 tiles of a product (counted for x_rows). Arrays that are written overlap no others but, as said, the
  * residual (out or pre at the base of x, or pre at that of out or the
@@ -694,7 +695,8 @@ size_t moe_expert_linear_backward_workspace_bytes(int W, int P, int64_t K, int64
  *   d_weight = d_pre^T . x            (over the expert's rows; 0 if it has none)
  *   d_bias   = sum of d_pre           (over the expert's rows, before d_pre's
  *                                      rounding, in a fixed order)
- * The products read the rounded d_pre, as they would between two layers.
+ * The products read the rounded d_pre, as they would between two layers (in
+ * fp16 a d_pre past 65504 is infinite there).
  *   x, x_rows, expert_offsets, weight, type, act   as moe_expert_linear
  *   pre, d_pre     host arrays of W device [x_rows[d]][NW]; both NULL with
  *                  A2AV_ACT_NONE, where d_pre is d_out

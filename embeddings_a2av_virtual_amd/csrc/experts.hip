@@ -376,7 +376,8 @@ __global__ __launch_bounds__(256) void k_expert_any(const ExpertArgs a) {
 // LDS and 1.9 GB of stores).
 //
 // Other shapes at 16384 rows, same box, all three products (forward / d_x /
-// d_weight, us through): eight waves and two stages of 64 with one barrier a step 848 / 849 / spills; two groups of waves in turn at reading and
+// d_weight, us through): eight waves and two stages of 64 with one barrier a
+// step 848 / 849 / spills; two groups of waves in turn at reading and
 // multiplying 928 / 778 / 852; four stages of 32, whose 64-byte requests double
 // the L2's work, 920 / 834 / 755; four waves of 128 x 128, half the LDS reads
 // but no second wave to issue beside a stalled one, 889 / 818 / 825; this one

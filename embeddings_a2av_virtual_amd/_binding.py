@@ -32,6 +32,9 @@ __all__ = [
     "moe_combine_backward", "moe_combine_return_backward_workspace_bytes",
     "moe_combine_return_backward", "moe_expert_linear_workspace_bytes", "moe_expert_linear",
     "moe_expert_linear_backward_workspace_bytes", "moe_expert_linear_backward",
+    "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_rms_norm",
+    "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
+    "moe_expert_linear_mx_workspace_bytes", "moe_expert_linear_mx", "MX_FP8", "MX_FP4",
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_SILU",
     "ACT_SWIGLU", "MAX_WIDTH",
     "keys_bucketize_workspace_bytes",
@@ -59,6 +62,7 @@ ST_BAD_PERM = 32
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU, ACT_SWIGLU = range(5)
 MAX_WIDTH = 1 << 20
+MX_FP8, MX_FP4 = 3, 4
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _lib = None
@@ -137,6 +141,20 @@ def lib():
         L.moe_expert_linear_backward_workspace_bytes.restype = sz
         L.moe_expert_linear_backward.argtypes = [i32, i32, i64, i64, i32, i32, vpp, i64p, vp, vpp,
                                                  vpp, vpp, vpp, vpp, vpp, vpp, vp, sz, vp, vp]
+        L.moe_mx_row_bytes.argtypes = [i32, i64]
+        L.moe_mx_row_bytes.restype = sz
+        L.moe_mx_quantize.argtypes = [i32, i64, i32, i32, vpp, i64p, vpp, vp, vp]
+        L.moe_mx_dequantize.argtypes = [i32, i64, i32, i32, vpp, i64p, vpp, vp, vp]
+        L.moe_rms_norm.argtypes = [i32, i64, i64, i32, ctypes.c_double, vpp, vpp, vp, vpp, vpp, vpp,
+                                   i32, vp, vp]
+        L.moe_rms_norm_backward_workspace_bytes.argtypes = [i32, i64, i64]
+        L.moe_rms_norm_backward_workspace_bytes.restype = sz
+        L.moe_rms_norm_backward.argtypes = [i32, i64, i64, i32, ctypes.c_double, vpp, vp, vpp, vpp,
+                                            vpp, vp, vp, sz, vp, vp]
+        L.moe_expert_linear_mx_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i64p]
+        L.moe_expert_linear_mx_workspace_bytes.restype = sz
+        L.moe_expert_linear_mx.argtypes = [i32, i32, i64, i64, i32, i32, vpp, i64p, vp, vpp, vpp,
+                                           vpp, i32, vp, sz, vp, vp]
         L.keys_bucketize_workspace_bytes.argtypes = [i32, i32]
         L.keys_bucketize_workspace_bytes.restype = sz
         L.keys_bucketize.argtypes = [i32, i32, i64, vpp, vpp, i64p, vpp, vpp, vp, vp, vp, sz, vp,
@@ -155,7 +173,8 @@ def lib():
                   "moe_combine_grouped", "moe_pack_dispatch", "moe_unpack_return",
                   "moe_combine_return", "moe_route", "moe_route_backward",
                   "moe_combine_backward", "moe_combine_return_backward", "moe_expert_linear",
-                  "moe_expert_linear_backward",
+                  "moe_expert_linear_backward", "moe_mx_quantize", "moe_mx_dequantize",
+                  "moe_rms_norm", "moe_rms_norm_backward", "moe_expert_linear_mx",
                   "keys_bucketize", "keys_exchange", "keys_exchange_noalloc",
                   "a2av_device_copy", "a2av_device_read", "a2av_device_fill"):
             getattr(L, f).restype = i32
@@ -592,6 +611,107 @@ def moe_expert_linear_backward(W, P, K, N, act, x, x_rows, expert_offsets, weigh
           _typed(d_out, "d_out", dtype, [int(n) * N for n in x_rows]),
           _typed(d_pre, "d_pre", dtype, wide), _typed(d_x, "d_x", dtype, xs),
           _typed(d_weight, "d_weight", dtype, ws), _typed(d_bias, "d_bias", dtype, [P * NW] * W),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"))
+
+
+def moe_mx_row_bytes(format, H) -> int:
+    return int(lib().moe_mx_row_bytes(int(format), int(H)))
+
+
+def _value_type(lists, name):
+    """The type of the first tensor in lists of fp32, bf16 or fp16 arrays."""
+    for t in lists:
+        if isinstance(t, torch.Tensor):
+            if t.dtype not in _TYPES:
+                raise ValueError(f"{name} must be fp32, bf16 or fp16, not {t.dtype}")
+            return t.dtype
+    raise ValueError(f"{name} must be a list of tensors, one per rank")
+
+
+def moe_mx_quantize(W, H, format, x, n_rows, rows, status, stream=None):
+    """Values [n_rows[r], H] (fp32, bf16 or fp16) to microscaled rows (uint8
+    [n_rows[r], moe_mx_row_bytes(format, H)]) of MX_FP8 or MX_FP4 elements."""
+    dtype, wide = _value_type(x, "x"), moe_mx_row_bytes(format, H)
+    if len(n_rows) != W:
+        raise ValueError("n_rows needs W entries")
+    _call("moe_mx_quantize", status, stream, int(W), int(H), _TYPES[dtype], int(format),
+          _typed(x, "x", dtype, [int(n) * H for n in n_rows]), _i64_array(n_rows),
+          _typed(rows, "rows", torch.uint8, [int(n) * wide for n in n_rows]),
+          _dev(status, "status"))
+
+
+def moe_mx_dequantize(W, H, format, rows, n_rows, out, status, stream=None):
+    """Microscaled rows back to values of out's type (fp32, bf16 or fp16)."""
+    dtype, wide = _value_type(out, "out"), moe_mx_row_bytes(format, H)
+    if len(n_rows) != W:
+        raise ValueError("n_rows needs W entries")
+    _call("moe_mx_dequantize", status, stream, int(W), int(H), _TYPES[dtype], int(format),
+          _typed(rows, "rows", torch.uint8, [int(n) * wide for n in n_rows]), _i64_array(n_rows),
+          _typed(out, "out", dtype, [int(n) * H for n in n_rows]), _dev(status, "status"))
+
+
+def moe_rms_norm(W, T, H, eps, x, residual, weight, sum, out, rows, format, status, stream=None):
+    """h = x + residual and y = h / sqrt(mean(h^2) + eps) * weight for rows
+    [T, H] per rank (fp32, bf16 or fp16): h into sum, y into out and, as
+    microscaled rows of the format, into rows. residual, sum, out and rows may
+    be None (out and rows not both)."""
+    dtype, n = _value_type([weight], "weight"), [T * H] * W
+    _call("moe_rms_norm", status, stream, int(W), int(T), int(H), _TYPES[dtype], float(eps),
+          _typed(x, "x", dtype, n), _typed(residual, "residual", dtype, n),
+          _one(weight, "weight", dtype, H), _typed(sum, "sum", dtype, n),
+          _typed(out, "out", dtype, n),
+          _typed(rows, "rows", torch.uint8, [T * moe_mx_row_bytes(format, H)] * W), int(format),
+          _dev(status, "status"))
+
+
+def moe_rms_norm_backward_workspace_bytes(W, T, H) -> int:
+    return int(lib().moe_rms_norm_backward_workspace_bytes(int(W), int(T), int(H)))
+
+
+def moe_rms_norm_backward(W, T, H, eps, x, weight, d_out, d_sum, d_x, d_weight, workspace, status,
+                          stream=None):
+    """The gradients of moe_rms_norm in its rows (d_x, of x and of the residual
+    alike) and its weight (d_weight, fp32 [H] over all ranks, or None); x is
+    the sum that it wrote, d_sum that sum's gradient by other ways or None."""
+    dtype, n = _value_type([weight], "weight"), [T * H] * W
+    _call("moe_rms_norm_backward", status, stream, int(W), int(T), int(H), _TYPES[dtype],
+          float(eps), _typed(x, "x", dtype, n), _one(weight, "weight", dtype, H),
+          _typed(d_out, "d_out", dtype, n), _typed(d_sum, "d_sum", dtype, n),
+          _typed(d_x, "d_x", dtype, n),
+          None if d_weight is None else _one(d_weight, "d_weight", torch.float32, H),
+          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+          _dev(status, "status"))
+
+
+def moe_expert_linear_mx_workspace_bytes(W, P, K, N, act, x_rows) -> int:
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    return int(lib().moe_expert_linear_mx_workspace_bytes(int(W), int(P), int(K), int(N), int(act),
+                                                          _i64_array(x_rows)))
+
+
+def moe_expert_linear_mx(W, P, K, N, x_format, act, x, x_rows, expert_offsets, weight, bias, out,
+                         workspace, status, stream=None):
+    """out = act(x . weight^T + bias) for the rows of every expert: x in
+    microscaled rows of x_format, the weight in MX_FP4 rows (uint8), bias fp32
+    or None, out bf16, fp16 or (uint8) rows of MX_FP8."""
+    NW = 2 * N if act == ACT_SWIGLU else N
+    if len(x_rows) != W:
+        raise ValueError("x_rows needs W entries")
+    first = next((t for t in out if isinstance(t, torch.Tensor)), None)
+    dtype = torch.bfloat16 if first is None else first.dtype
+    if dtype not in (torch.bfloat16, torch.float16, torch.uint8):
+        raise ValueError(f"out must be bf16, fp16 or uint8 (microscaled rows), not {dtype}")
+    wide = moe_mx_row_bytes(MX_FP8, N) if dtype == torch.uint8 else N
+    _call("moe_expert_linear_mx", status, stream, int(W), int(P), int(K), int(N), int(x_format),
+          int(act),
+          _typed(x, "x", torch.uint8, [int(n) * moe_mx_row_bytes(x_format, K) for n in x_rows]),
+          _i64_array(x_rows), _one(expert_offsets, "expert_offsets", torch.int64, W * (P + 1)),
+          _typed(weight, "weight", torch.uint8, [P * NW * moe_mx_row_bytes(MX_FP4, K)] * W),
+          _typed(bias, "bias", torch.float32, [P * NW] * W),
+          _typed(out, "out", dtype, [int(n) * wide for n in x_rows]),
+          MX_FP8 if dtype == torch.uint8 else _TYPES[dtype],
           _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
           _dev(status, "status"))
 

@@ -721,6 +721,159 @@ int moe_expert_linear_backward(int W, int P, int64_t K, int64_t N, int type, int
                                void *const *d_bias, void *workspace, size_t workspace_bytes,
                                int32_t *status, hipStream_t stream);
 
+/* microscaled row formats: elements of 8 or 4 bits in blocks of 32 */
+#define A2AV_MX_FP8 3 /* e4m3 elements (largest 448) */
+#define A2AV_MX_FP4 4 /* e2m1 elements (largest 6)   */
+
+/*
+ * Bytes of a microscaled row of H values (0 for invalid arguments). The row
+ * holds Hp elements, H rounded up to a multiple of 256, the last Hp - H of
+ * them 0: with A2AV_MX_FP8 a byte each, with A2AV_MX_FP4 two a byte, the even
+ * one in the low half. Behind them lie Hp / 32 scale bytes, one for every 32
+ * elements: element i stands for e_i * 2^(b - 127), b the byte of its block
+ * (255: NaN). The rest, up to the next multiple of 128 bytes, is unused. A
+ * row carries its scales with it: moe_pack_dispatch and the other exchanges
+ * move microscaled rows as rows of this many bytes.
+ *   H   1 .. A2AV_MAX_WIDTH
+ */
+size_t moe_mx_row_bytes(int format, int64_t H);
+
+/*
+ * Values to microscaled rows, for all W ranks. With m the largest magnitude
+ * of a block of 32 (the last block of a row may be short),
+ *   b = max(0, floor(log2 m) + 127 - 8)   A2AV_MX_FP8
+ *   b = max(0, floor(log2 m) + 127 - 2)   A2AV_MX_FP4
+ *   e_i = x_i / 2^(b - 127), to nearest even, at most 448 or 6 in magnitude
+ * A block of zeros has b = 0; one with an infinity or NaN has b = 255 and
+ * elements 0. The padding's elements and scale bytes are written as 0, the
+ * unused bytes are not written.
+ *   type         A2AV_DT_* of x
+ *   format       A2AV_MX_FP8 or A2AV_MX_FP4
+ *   x[W]         device [n_rows[r]][H] per rank (host n_rows; up to 2^31 - 1
+ *                pieces of 256 elements)
+ *   rows[W]      device [n_rows[r]][moe_mx_row_bytes(format, H)], written;
+ *                16-byte-aligned (else A2AV_EARG)
+ *   status       only read
+ * Arrays that are written overlap no others. One kernel.
+ */
+int moe_mx_quantize(int W, int64_t H, int type, int format, const void *const *x,
+                    const int64_t *n_rows, void *const *rows, int32_t *status,
+                    hipStream_t stream);
+
+/*
+ * Microscaled rows back to values, e_i * 2^(b - 127) rounded once to the type
+ * (in fp16 past 65504 infinite). Arguments as moe_mx_quantize, with rows[W]
+ * read (16-byte-aligned) and out[W] device [n_rows[r]][H] written.
+ */
+int moe_mx_dequantize(int W, int64_t H, int type, int format, const void *const *rows,
+                      const int64_t *n_rows, void *const *out, int32_t *status,
+                      hipStream_t stream);
+
+/*
+ * The root-mean-square norm in front of the router and the dispatch, with the
+ * addition of the residual before it, for all W ranks: for every row
+ *   h = x + residual, in fp32, rounded to type   (residual NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight        (in double)
+ *   sum = h,  out = y rounded to type,  rows = y as a microscaled row
+ * (y is rounded once into either; moe_mx_quantize says how blocks are made).
+ *   H             1 .. A2AV_MAX_WIDTH;  T up to 2^30
+ *   type          A2AV_DT_* of x, residual, weight, sum and out
+ *   eps           at least 0
+ *   x[W]          device [T][H] per rank
+ *   residual      host array of W device [T][H], or NULL
+ *   weight        device [H], shared by the ranks
+ *   sum           host array of W device [T][H], written, or NULL; only with
+ *                 a residual
+ *   out           host array of W device [T][H], written, or NULL
+ *   rows          host array of W device [T][moe_mx_row_bytes(format, H)],
+ *                 written, 16-byte-aligned, or NULL; out or rows is wanted
+ *   format        A2AV_MX_FP8 or A2AV_MX_FP4
+ *   status        only read
+ * sum and out may each be x or the residual, but not one array; other arrays
+ * that are written overlap no others (rows at the base of any, sum at that of
+ * out: A2AV_EARG). One kernel; widths that are multiples of 8 up to 32768 at
+ * 16-byte-aligned bases are read once.
+ */
+int moe_rms_norm(int W, int64_t T, int64_t H, int type, double eps, const void *const *x,
+                 const void *const *residual, const void *weight, void *const *sum,
+                 void *const *out, void *const *rows, int format, int32_t *status,
+                 hipStream_t stream);
+
+/*
+ * Workspace bytes moe_rms_norm_backward needs (0 for invalid sizes).
+ */
+size_t moe_rms_norm_backward_workspace_bytes(int W, int64_t T, int64_t H);
+
+/*
+ * The gradient of moe_rms_norm from d_out, that of its y, and d_sum, that of
+ * its h by other ways (NULL: none). With r = 1 / sqrt(mean(h^2) + eps),
+ *   d_x = r * (d_out * weight - h * r^2 * mean(d_out * weight * h)) + d_sum
+ *   d_weight = sum over the rows of all ranks of d_out * h * r
+ * d_x is the gradient of x and of the residual alike. The row's sums are in
+ * double, the rest in fp32, d_x rounded once; d_weight is summed in a fixed
+ * order (0 without rows). What rounds y to 8 or 4 bits has no gradient of its
+ * own here: d_out is taken as y's.
+ *   x[W]        device [T][H] of type: h, moe_rms_norm's sum (or its x)
+ *   d_out[W]    device [T][H] of type
+ *   d_sum       host array of W device [T][H] of type, or NULL
+ *   d_x[W]      device [T][H] of type, written; may be x, d_out or d_sum
+ *   d_weight    device fp32 [H], written, or NULL: not wanted
+ *   workspace   device scratch of >= moe_rms_norm_backward_workspace_bytes(),
+ *               16-byte-aligned
+ *   status      only read
+ * Other arrays that are written overlap no others. Two kernels, or one
+ * without d_weight.
+ */
+int moe_rms_norm_backward(int W, int64_t T, int64_t H, int type, double eps,
+                          const void *const *x, const void *weight, const void *const *d_out,
+                          const void *const *d_sum, void *const *d_x, float *d_weight,
+                          void *workspace, size_t workspace_bytes, int32_t *status,
+                          hipStream_t stream);
+
+/*
+ * Workspace bytes moe_expert_linear_mx needs (0 for invalid sizes): x_rows as
+ * below (host).
+ */
+size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, int act,
+                                            const int64_t *x_rows);
+
+/*
+ * moe_expert_linear on microscaled rows with 4-bit weights: expert j of rank d
+ * has rows expert_offsets[d][j] .. [j+1] of x[d], and
+ *   h = x[d][row] . weight[d][j]^T + bias[d][j]     (fp32 sums)
+ *   out[d][row] = act(h), rounded once
+ * with A2AV_ACT_SWIGLU as moe_expert_linear has it (2N weight rows, N outputs).
+ * The products read the elements as they lie: a block that stands for NaN gives
+ * NaN where its row or column goes.
+ *   K, N            1 .. A2AV_MAX_WIDTH
+ *   x_format        A2AV_MX_FP8 or A2AV_MX_FP4, of x
+ *   x[W]            device [x_rows[d]][moe_mx_row_bytes(x_format, K)] (host
+ *                   x_rows, at most 2^30), 16-byte-aligned
+ *   expert_offsets  device int64 [W][P+1]; W * P <= A2AV_MAX_EXPERTS
+ *   weight[W]       device [P][NW][moe_mx_row_bytes(A2AV_MX_FP4, K)] (NW = 2N
+ *                   with SwiGLU, else N), 16-byte-aligned: moe_mx_quantize of
+ *                   [P * NW][K]
+ *   bias            host array of W device fp32 [P][NW], or NULL
+ *   out[W]          written below the rank's total; by out_type:
+ *                   A2AV_DT_BF16, A2AV_DT_F16   device [x_rows[d]][N]
+ *                   A2AV_MX_FP8   device [x_rows[d]][moe_mx_row_bytes(
+ *                                 A2AV_MX_FP8, N)], 16-byte-aligned: the x of
+ *                                 a product over N, from fp32 values
+ *   workspace       device scratch of at least
+ *                   moe_expert_linear_mx_workspace_bytes()
+ *   status          as moe_expert_linear; nothing but the workspace is written
+ *                   on failure
+ * Arrays that are written overlap no others (out at the base of x: A2AV_EARG).
+ * Two kernels: the plan of moe_expert_linear, and the products on matrix cores;
+ * their tiles are chosen for as many rows as x_rows allows.
+ */
+int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_format, int act,
+                         const void *const *x, const int64_t *x_rows,
+                         const int64_t *expert_offsets, const void *const *weight,
+                         const float *const *bias, void *const *out, int out_type,
+                         void *workspace, size_t workspace_bytes, int32_t *status,
+                         hipStream_t stream);
+
 /*
  * Workspace bytes keys_bucketize needs (0 for invalid sizes).
  */

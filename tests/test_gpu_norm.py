@@ -1,0 +1,294 @@
+"""The norm in front of the router and its gradient against 64 bits: every type
+and combination of outputs, widths from 1 to more than the register kernels
+take, bases that are no 16-byte multiples, arrays in place, extreme rows and
+refusals."""
+import math
+
+import pytest
+import torch
+
+import layer_ref as R
+import mx_ref as M
+from embeddings_a2av_virtual_amd import _binding as B
+from gpu_util import GuardedBuffer, SENT
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+EPS = 1e-6
+
+
+def _array(shape, dtype, pad=0, of=None):
+    n = dtype.itemsize
+    for s in shape:
+        n *= s
+    b = GuardedBuffer(n, pad=pad)
+    v = b.view.view(dtype).reshape(shape)
+    if of is not None:
+        v.copy_(of)
+    return b, v
+
+
+def norm(xs, rs, weight, form=None, want_sum=True, want_out=True, pad=0, place=None, eps=EPS, status=0):
+    """sum, out and microscaled rows of every rank; place: which input sum and
+    out are written over."""
+    W, (T, H), t = len(xs), xs[0].shape, xs[0].dtype
+    x = [_array((T, H), t, pad, v)[1] for v in xs]
+    r = None if rs is None else [_array((T, H), t, pad, v)[1] for v in rs]
+    bufs = {"sum": [_array((T, H), t, pad) for _ in xs], "out": [_array((T, H), t, pad) for _ in xs],
+            "rows": [_array((T, M.row_bytes(form or M.FP8, H)), torch.uint8) for _ in xs]}
+    arg = {k: [v for _, v in b] for k, b in bufs.items()}
+    if place:
+        arg["sum"], arg["out"] = ({"x": x, "r": r}[p] if p else arg[k] for k, p in zip(("sum", "out"), place))
+    st = torch.full((1,), status, dtype=torch.int32, device="cuda")
+    B.moe_rms_norm(W, T, H, eps, x, r, _array((H,), t, pad, weight)[1], arg["sum"] if rs and want_sum else None,
+                   arg["out"] if want_out else None, arg["rows"] if form else None, form or B.MX_FP8, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == status and all(b.guards_intact() for v in bufs.values() for b, _ in v)
+    return {k: [v.cpu() for v in a] for k, a in arg.items()}
+
+
+def _blocks(got, want, form, H):
+    """Which blocks of the rows differ, in their elements or their scale."""
+    n = M.padded(H) // (1 if form == M.FP8 else 2)
+    off = (got != want)
+    return off[:, :n].reshape(len(got), M.padded(H) // 32, -1).any(-1) | off[:, n:]
+
+
+def check(xs, rs, weight, form=None, eps=EPS, **kw):
+    got = norm(xs, rs, weight, form, eps=eps, **kw)
+    t, H = xs[0].dtype, xs[0].shape[1]
+    half, tiny = R.half_step(t), torch.finfo(t).smallest_normal * R.half_step(t) * 2
+    for d, x in enumerate(xs):
+        h = M.add(x, None if rs is None else rs[d])
+        y = M.norm(h, weight, eps)
+        if rs is not None and kw.get("want_sum", True):
+            assert torch.equal(got["sum"][d], h)
+        if kw.get("want_out", True):
+            # y in double, then fp32, then the type: half a step of each
+            far = (got["out"][d].double() - y).abs() > y.abs() * (half + 2.0 ** -23) + tiny
+            assert not far.any(), far.nonzero()[:4].tolist()
+        if form:
+            n = M.used_bytes(form, H)
+            # the H squares' sum, the root, the quotient and two products in double leave a
+            # relative (H / 2 + 6) * 2^-53 on either side: what that moves over a border (the
+            # rows of 65504 and eps 1e-6, whose y is 1 - 1.2e-16) may be on both
+            by = (H / 2 + 6) * 2.0 ** -53 * 2
+            bad = torch.ones(y.shape[0], M.padded(H) // 32, dtype=torch.bool)
+            for f in (0, -by, by):
+                bad &= _blocks(got["rows"][d][:, :n], M.quantize(y * (1 + f), form), form, H)
+            assert not bad.any(), bad.nonzero()[:4].tolist()
+            assert (got["rows"][d][:, n:] == SENT).all()
+
+
+def _rows(g, W, T, H, t):
+    return [(torch.randn(T, H, generator=g) * torch.exp(torch.randn(T, 1, generator=g))).to(t) for _ in range(W)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H", [1, 5, 8, 31, 40, 264, 1003, 2048, 2056, 4104, 7168, 8200, 16392, 32768, 32776])
+def test_norm(kind, H):
+    g = torch.Generator().manual_seed(H)
+    t, W, T = TYPES[kind], 2, 3
+    weight = (1 + 0.2 * torch.randn(H, generator=g)).to(t)
+    xs, rs = _rows(g, W, T, H, t), _rows(g, W, T, H, t)
+    check(xs, rs, weight, M.FP8)
+    check(xs, None, weight, M.FP4)
+    check(xs, rs, weight, M.FP4, want_sum=False, want_out=False)
+    check(xs, None, weight)
+    check(xs, rs, weight, M.FP8, pad=t.itemsize)
+
+
+@pytest.mark.parametrize("T", [1, 2, 700])
+@pytest.mark.parametrize("H", [1003, 4096])
+def test_many_rows(T, H):
+    g = torch.Generator().manual_seed(T)
+    weight = (1 + 0.2 * torch.randn(H, generator=g)).to(torch.bfloat16)
+    check(_rows(g, 3, T, H, torch.bfloat16), _rows(g, 3, T, H, torch.bfloat16), weight, M.FP8)
+
+
+@pytest.mark.parametrize("H", [256, 1003])
+@pytest.mark.parametrize("place", [("x", ""), ("r", ""), ("", "x"), ("", "r"), ("x", "r"), ("r", "x")])
+def test_in_place(H, place):
+    g = torch.Generator().manual_seed(3)
+    weight = torch.randn(H, generator=g).to(torch.bfloat16)
+    check(_rows(g, 2, 4, H, torch.bfloat16), _rows(g, 2, 4, H, torch.bfloat16), weight, M.FP8, place=place)
+
+
+@pytest.mark.parametrize("H", [64, 63])
+def test_extreme_rows(H):
+    """Rows of zeros, of the largest and smallest values, with infinities and NaN."""
+    for t in TYPES.values():
+        top, tiny = torch.finfo(t).max, torch.finfo(t).smallest_normal
+        x = torch.ones(6, H, dtype=t)
+        x[0], x[1], x[2] = 0, top, tiny
+        x[3, 1:], x[3, 0] = tiny, top / 4
+        x[4], x[5] = -top / 2, tiny / 4
+        w = torch.ones(H, dtype=t)
+        for eps in (0.0, 1e-6):
+            check([x[1:] if eps == 0 else x], None, w, M.FP8, eps=eps)
+        for bad in (math.inf, -math.inf, math.nan):
+            y = torch.ones(2, H, dtype=t)
+            y[0, 3] = bad
+            got = norm([y], None, w, M.FP8)
+            assert torch.isnan(got["out"][0][0, 3]) and torch.isnan(M.values(got["rows"][0][:1], M.FP8, 32)).all()
+            assert torch.isnan(got["out"][0][0]).all() == math.isnan(bad)  # h / infinity is 0
+            assert torch.isfinite(got["out"][0][1]).all()
+        got = norm([x[:1]], None, w, M.FP8, eps=0.0)  # 0 / 0
+        assert torch.isnan(got["out"][0]).all()
+
+
+def test_no_rows_and_a_set_status():
+    w = torch.ones(64)
+    norm([torch.zeros(0, 64)], [torch.zeros(0, 64)], w, M.FP8)
+    got = norm([torch.ones(2, 64)], [torch.ones(2, 64)], w, M.FP8, status=4)
+    assert all((v[0].view(torch.uint8) == SENT).all() for v in got.values())
+
+
+def test_refusals():
+    x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(64, device="cuda")
+    rows, st = torch.zeros(4, 384, dtype=torch.uint8, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ok = dict(W=1, T=4, H=64, eps=EPS, x=[x], residual=None, weight=w, sum=None, out=[x.clone()], rows=[rows], format=3,
+              status=st)
+    for kw in (dict(x=[x, x]), dict(T=5), dict(H=65), dict(weight=w.half()), dict(weight=w.double()), dict(x=[x.half()]),
+               dict(out=None, rows=None), dict(sum=[x.clone()]), dict(rows=[rows.float()]), dict(rows=[rows[:3]]),
+               dict(rows=[rows.flatten()[8:]], T=3), dict(format=0), dict(eps=-1.0), dict(x=[x.cpu()]),
+               dict(x=[torch.zeros(64, 4, device="cuda").t()])):
+        with pytest.raises((ValueError, B.A2avError)):
+            B.moe_rms_norm(**{**ok, **kw})
+    B.moe_rms_norm(**ok)
+
+
+@pytest.mark.parametrize("grid", [1, 5])
+def test_small_grids(grid, monkeypatch):
+    monkeypatch.setenv("A2AV_MAX_GRID", str(grid))
+    g = torch.Generator().manual_seed(grid)
+    for H in (264, 1003):
+        check(_rows(g, 2, 9, H, torch.float16), _rows(g, 2, 9, H, torch.float16), torch.ones(H).half(), M.FP8)
+
+
+# ------------------------------------------------------------------ gradient
+def grad(hs, weight, gs, ds, want_w=True, pad=0, place=None, eps=EPS, status=0):
+    W, (T, H), t = len(hs), hs[0].shape, hs[0].dtype
+    arg = {k: None if v is None else [_array((T, H), t, pad, x)[1] for x in v] for k, v in
+           (("x", hs), ("d_out", gs), ("d_sum", ds))}
+    bufs = [_array((T, H), t, pad) for _ in hs]
+    d_x = arg[place] if place else [v for _, v in bufs]
+    wb, d_w = _array((H,), torch.float32)
+    st = torch.full((1,), status, dtype=torch.int32, device="cuda")
+    ws = torch.empty(B.moe_rms_norm_backward_workspace_bytes(W, T, H), dtype=torch.uint8, device="cuda").random_()
+    B.moe_rms_norm_backward(W, T, H, eps, arg["x"], _array((H,), t, pad, weight)[1], arg["d_out"], arg["d_sum"], d_x,
+                            d_w if want_w else None, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == status and all(b.guards_intact() for b, _ in bufs) and wb.guards_intact()
+    return [x.cpu() for x in d_x], d_w.cpu()
+
+
+def check_grad(hs, weight, gs, ds, eps=EPS, **kw):
+    got, got_w = grad(hs, weight, gs, ds, eps=eps, **kw)
+    t, H, rows = hs[0].dtype, hs[0].shape[1], len(hs) * len(hs[0])
+    half, tiny, f = R.half_step(t), torch.finfo(t).smallest_normal * R.half_step(t) * 2, 2.0 ** -24
+    want_w, mag_w = torch.zeros(H, dtype=torch.float64), torch.zeros(H, dtype=torch.float64)
+    for d, h in enumerate(hs):
+        want, dw = M.norm_grad(h, weight, eps, gs[d], None if ds is None else ds[d])
+        v, g = h.double(), gs[d].double()
+        r = 1 / torch.sqrt((v * v).mean(-1, keepdim=True) + eps)
+        gw = g * weight.double()
+        m = (r * r * (gw * v).mean(-1, keepdim=True)).abs()
+        # fp32: r and m rounded, the two products, their difference, the product
+        # with r, the addition; then the type
+        mag = r * (gw.abs() + v.abs() * m)
+        err = 6 * f * mag + 2 * f * (0 if ds is None else ds[d].double().abs())
+        far = (got[d].double() - want).abs() > err + want.abs() * half * 1.01 + tiny
+        assert not far.any(), (d, far.nonzero()[:4].tolist())
+        want_w, mag_w = want_w + dw, mag_w + (g * v * r).abs().sum(0)
+    if kw.get("want_w", True):
+        # r, two products and then sums: over a group's rows, 32 groups and 16 runs of them
+        n = -(-rows // 512) + 32 + 16 + 4
+        far = (got_w.double() - want_w).abs() > n * f * mag_w
+        assert not far.any(), far.nonzero()[:4].tolist()
+    else:
+        assert (got_w.view(torch.uint8) == SENT).all()
+    return got, got_w
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H", [1, 5, 8, 40, 264, 1003, 2056, 4104, 7168, 8200, 16392, 32776])
+def test_gradient(kind, H):
+    g = torch.Generator().manual_seed(H)
+    t, W, T = TYPES[kind], 2, 5
+    weight = (1 + 0.2 * torch.randn(H, generator=g)).to(t)
+    hs, gs, ds = (_rows(g, W, T, H, t) for _ in range(3))
+    check_grad(hs, weight, gs, ds)
+    check_grad(hs, weight, gs, None, want_w=False)
+    check_grad(hs, weight, gs, None, pad=t.itemsize)
+
+
+@pytest.mark.parametrize("H", [64, 1003])
+@pytest.mark.parametrize("T", [1, 511, 512, 1300])
+def test_gradient_of_many_rows(T, H):
+    g = torch.Generator().manual_seed(T)
+    weight = (1 + 0.2 * torch.randn(H, generator=g)).to(torch.bfloat16)
+    hs, gs, ds = (_rows(g, 2, T, H, torch.bfloat16) for _ in range(3))
+    first = check_grad(hs, weight, gs, ds)
+    again = grad(hs, weight, gs, ds)
+    assert torch.equal(first[1], again[1]) and all(torch.equal(a, b) for a, b in zip(first[0], again[0]))
+
+
+@pytest.mark.parametrize("H", [256, 1003])
+@pytest.mark.parametrize("place", ["x", "d_out", "d_sum"])
+def test_gradient_in_place(H, place):
+    g = torch.Generator().manual_seed(4)
+    weight = torch.randn(H, generator=g)
+    hs, gs, ds = (_rows(g, 2, 6, H, torch.float32) for _ in range(3))
+    check_grad(hs, weight, gs, ds, place=place)
+
+
+def test_gradient_against_differences():
+    """The forward pass's own fp32 outputs, weighted and summed in 64 bits, along one direction."""
+    g = torch.Generator().manual_seed(5)
+    H = 24
+    h, w, d, v = (torch.randn(3, H, generator=g) for _ in range(4))
+    w, step = w[0], 1e-2
+    d_x, d_w = grad([h], w, [d], None, eps=1e-3)
+    f = lambda x, u: float((norm([x], None, u, eps=1e-3)["out"][0].double() * d.double()).sum())  # noqa: E731
+    along = (f(h + step * v, w) - f(h - step * v, w)) / (2 * step)
+    # third derivatives of order 1 over 72 terms, times step^2 / 6; fp32 outputs over 2 * step
+    assert abs(along - float((d_x[0].double() * v.double()).sum())) < 72 * (step ** 2 + 2.0 ** -23 / step)
+    u = v[0]
+    along = (f(h, w + step * u) - f(h, w - step * u)) / (2 * step)
+    assert abs(along - float((d_w.double() * u.double()).sum())) < 72 * 4 * 2.0 ** -23 / step
+
+
+def test_gradient_without_rows_and_with_a_set_status():
+    w = torch.ones(64)
+    _, d_w = grad([torch.zeros(0, 64)] * 2, w, [torch.zeros(0, 64)] * 2, None)
+    assert (d_w == 0).all()
+    one = [torch.ones(2, 64)]
+    d_x, d_w = grad(one, w, one, one, status=2)
+    assert (d_x[0].view(torch.uint8) == SENT).all() and (d_w.view(torch.uint8) == SENT).all()
+
+
+def test_gradient_of_extreme_rows():
+    """Squares past fp32's range, and rows of zeros."""
+    for t in (torch.float32, torch.bfloat16):
+        h = torch.full((3, 40), 1e25, dtype=t)
+        h[1], h[2] = 0, 1e-25
+        h[0, ::2] *= -0.5
+        g = torch.ones(3, 40, dtype=t)
+        g[:, 1::3] = -2
+        check_grad([h], torch.ones(40, dtype=t), [g], None)
+
+
+def test_gradient_refusals():
+    x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(64, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(B.moe_rms_norm_backward_workspace_bytes(1, 4, 64), dtype=torch.uint8, device="cuda")
+    ok = dict(W=1, T=4, H=64, eps=EPS, x=[x], weight=w, d_out=[x.clone()], d_sum=None, d_x=[x.clone()],
+              d_weight=w.clone(), workspace=ws, status=st)
+    for kw in (dict(x=[x, x]), dict(T=5), dict(H=65), dict(weight=w.half()), dict(d_out=[x.half()]), dict(d_x=[x[:3]]),
+               dict(d_weight=w.half()), dict(d_weight=w[:63]), dict(workspace=ws[:-1]), dict(workspace=ws[8:]),
+               dict(d_out=None), dict(d_x=None), dict(eps=math.nan)):
+        with pytest.raises((ValueError, B.A2avError, TypeError)):
+            B.moe_rms_norm_backward(**{**ok, **kw})
+    B.moe_rms_norm_backward(**ok)

@@ -6,10 +6,11 @@
 // instructions take both operands as they lie and multiply by the scales, with
 // fp32 sums.
 //
-//   k_mx_plain   one 64 x 128 tile, operands straight from memory
+//   k_mx_tile   one tile, operands through LDS
 #include <hip/hip_runtime.h>
 
 #include <cstring>
+#include <utility>
 
 #include "experts.hpp"
 #include "mx.hpp"
@@ -38,14 +39,6 @@ struct MxExpertArgs {
     int wide;  // out and bias by 16-byte vectors
     int cols;  // column tiles
 };
-
-// The first operand's rows are the weight's (e2m1), the second's x's; a lane has
-// the fp32 sums of x row lane % 32 (or 16).
-template <int FORMAT>
-__device__ __forceinline__ f32x16 mfma32(i32x4 w, i32x8 x, f32x16 c, int sw, int sx) {
-    const i32x8 w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x, c, 4, FORMAT == A2AV_MX_FP8 ? 0 : 4, 0, sw, 0, sx);
-}
 
 // ------------------------------------------------------------------ epilogue
 // The sums of a wave leave through its part of LDS, so that one lane gets 8
@@ -137,65 +130,330 @@ __device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, i
     }
 }
 
-// ------------------------------------------------------------------ products
-// One 64 x 128 tile by four waves of 32 x 64; every lane loads its own 16 bytes
-// of each operand and the four scales of its row's 128 elements.
+// ------------------------------------------------------------------ the tiles
+// Tiles of BM rows and BC columns. LDS rows are 128 bytes of an operand's row: 256
+// elements of e2m1 or 128 of e4m3, so that a step is 256 elements of 4-bit rows or
+// 128 of 8-bit ones, and every second step of those takes new weights. Buffer
+// loads fill two stages of either operand; the eight 16-byte chunks of LDS row r
+// are permuted by r / 2, which puts the 16 lanes of rows r .. r + 15 in different
+// banks. Rows and elements outside are loaded out of the buffer's range, which
+// writes zeros.
+template <int ROWS, int WAVES>
+struct MxOperand {
+    static constexpr int kLoads = ROWS / 8 / WAVES;  // 16-byte loads a thread and stage
+    const unsigned char *base;
+    uint32_t span;         // bytes of the buffer: the tile's rows
+    uint32_t off[kLoads];  // of a thread's loads in the first stage
+    int at, end;           // byte of the next stage, and behind the last
+
+    // `rows` rows of `stride` bytes from p; a gated product takes blocks of 16 rows
+    // from p and p2 in turn (a wave's loads are all of the one or of the other).
+    __device__ __forceinline__ void init(const unsigned char *p, const unsigned char *p2, int64_t stride, int64_t rows,
+                                         int64_t bytes, int wave, int lane) {
+        static_assert(WAVES % 4 == 0, "");
+        const int64_t most = p2 ? ROWS / 2 : ROWS;
+        base = p2 && ((wave >> 1) & 1) ? p2 : p;
+        span = (uint32_t)((rows < 0 ? 0 : rows < most ? rows : most) * stride);
+        at = 0;
+        end = (int)bytes;
+        const int k = ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int r = (i * WAVES + wave) * 8;
+            off[i] = (uint32_t)((p2 ? (r >> 5) * 16 + (r & 8) : r) + (lane >> 3)) * (uint32_t)stride + k;
+        }
+    }
+    // Loads FROM .. TO of the next stage.
+    template <int FROM, int TO>
+    __device__ __forceinline__ void load(unsigned char *lds, int wave) const {
+        const rsrc_t b = buffer(base, at < end ? span : 0);
+#pragma unroll
+        for (int i = FROM; i < TO; i++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void *)(lds + (i * WAVES + wave) * 1024), 16, (int)off[i],
+                                                     at, 0, 0);
+    }
+    __device__ __forceinline__ void next() { at += 128; }
+};
+
+template <int FORMAT, int BM, int BC, int WM, int WC>
+struct MxShape {
+    static constexpr int kWaves = WM * WC, kThreads = kWaves * kWave;
+    static constexpr int kBlocksM = BM / WM / 32, kBlocksC = BC / WC / 32;
+    static constexpr int kQuarters = FORMAT == A2AV_MX_FP8 ? 2 : 4;  // of 64 elements in a step
+    static constexpr int kScaleRows = BM + BC;
+    static_assert(kScaleRows <= kThreads && kBlocksC == 2, "");
+    typedef MxOperand<BM, kWaves> A;
+    typedef MxOperand<BC, kWaves> B;
+};
+
+// The scales of a tile's rows, 1024 elements (32 bytes a row) at a time: one row of
+// x or of the weight per thread, through registers to the two LDS buffers. In LDS
+// the halves of 16 bytes lie apart, row after row.
+constexpr int kScaleMacros = 4;  // steps of 256 elements in a buffer
+
+template <typename S>
+struct MxScales {
+    const unsigned char *row;  // the thread's row's scales
+    int last;                  // offset of the last 16 bytes inside the row
+    u32x4 v[2];
+    __device__ __forceinline__ void load(int chunk) {
+        v[0] = *(const u32x4 *)(row + min(chunk * 32, last));
+        v[1] = *(const u32x4 *)(row + min(chunk * 32 + 16, last));
+    }
+    __device__ __forceinline__ void store(u32x4 *lds, int chunk) const {
+        if ((int)threadIdx.x >= S::kScaleRows) return;
+        lds += (chunk & 1) * 2 * S::kScaleRows + threadIdx.x;
+        lds[0] = v[0];
+        lds[S::kScaleRows] = v[1];
+    }
+};
+
+// One position: a block of 32 rows times the wave's 64 columns, 64 elements.
 template <int FORMAT>
-__global__ __launch_bounds__(256) void k_mx_plain(const MxExpertArgs a) {
-    __shared__ f32x4 sums[4][32 * 16];
+struct MxFrag {
+    typedef i32x8 type;
+};
+template <>
+struct MxFrag<A2AV_MX_FP4> {
+    typedef i32x4 type;
+};
+
+template <int FORMAT, int BYTE>
+__device__ __forceinline__ f32x16 mfma_at(i32x4 w, i32x8 x, f32x16 c, uint32_t sw, uint32_t sx) {
+    const i32x8 w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x, c, 4, FORMAT == A2AV_MX_FP8 ? 0 : 4, BYTE, (int)sw, BYTE,
+                                                           (int)sx);
+}
+template <int FORMAT, int BYTE>
+__device__ __forceinline__ f32x16 mfma_at(i32x4 w, i32x4 x, f32x16 c, uint32_t sw, uint32_t sx) {
+    return mfma_at<FORMAT, BYTE>(w, __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1), c, sw, sx);
+}
+
+// f of 0, 1, ... as constants.
+template <typename F, int... I>
+__device__ __forceinline__ void each(const F &f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+// The contraction of one tile with NB row blocks a wave (the blocks of the waves
+// alternate, so that a tile with few rows keeps all of them busy). The step's
+// positions follow each other quarter by quarter; the rows' fragments are read
+// kAhead positions ahead. kAhead positions before a step's end everything of its
+// stages has been read: one barrier there frees them for the loads of the step
+// after the next, and publishes the next one's.
+template <int FORMAT, int BM, int BC, int WM, int WC, int NB>
+__device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM, WC>::A &oa,
+                                            typename MxShape<FORMAT, BM, BC, WM, WC>::B &ob,
+                                            MxScales<MxShape<FORMAT, BM, BC, WM, WC>> &os, unsigned char *const (&sa)[2],
+                                            unsigned char *const (&sb)[2], u32x4 *ss, int macros,
+                                            f32x16 (&acc)[MxShape<FORMAT, BM, BC, WM, WC>::kBlocksM][2]) {
+    typedef MxShape<FORMAT, BM, BC, WM, WC> S;
+    typedef typename MxFrag<FORMAT>::type frag;
+    constexpr bool k8 = FORMAT == A2AV_MX_FP8;
+    constexpr int Q = S::kQuarters, P = Q * NB, kRing = NB >= 4 ? 4 : 2, kAhead = kRing - 1;
+    constexpr int kLoadsA = (NB * WM * 32 + S::kWaves * 8 - 1) / (S::kWaves * 8) < S::A::kLoads
+                                ? (NB * WM * 32 + S::kWaves * 8 - 1) / (S::kWaves * 8) : S::A::kLoads;
+    constexpr int kLoadsB = S::B::kLoads;
+    constexpr int kWords = k8 ? 1 : 2;  // of scales of a row and step
+    static_assert(P % kRing == 0 && kAhead <= NB, "");
+    const int lane = threadIdx.x & (kWave - 1), half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WC, wc = wave % WC;
+    int spot = (lane & 31) * 128 + ((half ^ ((lane >> 1) & 7)) << 4);  // of a row's first chunk
+    const auto read_a = [&](const unsigned char *s, int m, int q) __attribute__((always_inline)) -> frag {
+        const unsigned char *p = s + (m * WM + wm) * 32 * 128;
+        if constexpr (k8) {
+            const i32x4 lo = *(const i32x4 *)(p + (spot ^ q * 64)), hi = *(const i32x4 *)(p + (spot ^ (q * 64 + 32)));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *(const i32x4 *)(p + (spot ^ q * 32));
+        }
+    };
+    const auto read_b = [&](i32x4(&f)[2], const unsigned char *s, int q) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < 2; c++) f[c] = *(const i32x4 *)(s + (wc * 2 + c) * 32 * 128 + (spot ^ q * 32));
+    };
+    uint32_t wa[2][NB][kWords], wb[2][2][kWords];
+    const int scale_row = lane & 31, shift = half * 8;
+    // the scales of step `of` of macro step `macro`
+    const auto read_scales = [&](auto set, int macro, int of) __attribute__((always_inline)) {
+        constexpr int kSet = decltype(set)::value;
+        const uint32_t *p = (const uint32_t *)(ss + ((macro >> 1) & 3) * S::kScaleRows + scale_row) + (macro & 1) * 2 + of;
+        const auto get = [&](uint32_t(&w)[kWords], int row) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kWords; i++) w[i] = p[row * 4 + i];
+        };
+#pragma unroll
+        for (int m = 0; m < NB; m++) get(wa[kSet][m], (m * WM + wm) * 32);
+#pragma unroll
+        for (int c = 0; c < 2; c++) get(wb[kSet][c], BM + (wc * 2 + c) * 32);
+    };
+    const auto shift_scales = [&](auto set) __attribute__((always_inline)) {
+        constexpr int kSet = decltype(set)::value;
+#pragma unroll
+        for (int i = 0; i < kWords; i++) {
+#pragma unroll
+            for (int m = 0; m < NB; m++) wa[kSet][m][i] >>= shift;
+#pragma unroll
+            for (int c = 0; c < 2; c++) wb[kSet][c][i] >>= shift;
+        }
+    };
+    typedef std::integral_constant<int, 0> zero;
+    frag fa[kRing];
+    i32x4 fb[2][2];
+    os.load(0);
+    oa.template load<0, kLoadsA>(sa[0], wave);
+    ob.template load<0, kLoadsB>(sb[0], wave);
+    oa.next();
+    ob.next();
+    oa.template load<0, kLoadsA>(sa[1], wave);
+    ob.template load<0, kLoadsB>(sb[1], wave);
+    oa.next();
+    ob.next();
+    os.store(ss, 0);
+    wait_for<0, true>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_scales(zero{}, 0, 0);
+    read_b(fb[0], sb[0], 0);
+#pragma unroll
+    for (int p = 0; p < kAhead; p++) fa[p] = read_a(sa[0], p % NB, p / NB);
+    // step `i` of the unrolled ones (its stages by its number), in macro step `macro`
+    const auto step = [&](auto number, int macro) __attribute__((always_inline)) {
+        constexpr int i = decltype(number)::value;
+        constexpr int kStageA = i % 2, kStageB = k8 ? i / 2 % 2 : i % 2, kPart = k8 ? i % 2 : 0;
+        constexpr bool kFreesB = !k8 || i % 2 == 1;
+        constexpr int kNextB = kFreesB ? 1 - kStageB : kStageB, kFirstB = k8 && !kFreesB ? 2 : 0;
+        constexpr int kSet = i % 2;
+        shift_scales(std::integral_constant<int, kSet>{});
+        if constexpr (kPart == 0) {
+            if ((macro & (kScaleMacros - 1)) == 0) os.load(macro / kScaleMacros + 1);
+            if ((macro & (kScaleMacros - 1)) == 2) os.store(ss, macro / kScaleMacros + 1);
+        }
+        const auto position = [&](auto place) __attribute__((always_inline)) {
+            constexpr int p = decltype(place)::value, q = p / NB, m = p % NB, next = p + kAhead;
+            if constexpr (p == P - kAhead) {
+                wait_for<0, true>();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (next < P) fa[next % kRing] = read_a(sa[kStageA], next % NB, next / NB);
+            else fa[next % kRing] = read_a(sa[1 - kStageA], (next - P) % NB, (next - P) / NB);
+            if constexpr (m == 0 && q + 1 < Q) read_b(fb[(q + 1) & 1], sb[kStageB], kPart * 2 + q + 1);
+            if constexpr (p == P - kAhead) read_b(fb[0], sb[kNextB], kFirstB);
+            if constexpr (p == 0)
+                read_scales(std::integral_constant<int, 1 - kSet>{}, kFreesB ? macro + 1 : macro, k8 && !kFreesB ? 1 : 0);
+            if constexpr (p >= P - kAhead) {
+                constexpr int k = p - (P - kAhead);
+                oa.template load<kLoadsA * k / kAhead, kLoadsA *(k + 1) / kAhead>(sa[kStageA], wave);
+                if constexpr (kFreesB) ob.template load<kLoadsB * k / kAhead, kLoadsB *(k + 1) / kAhead>(sb[kStageB], wave);
+                if constexpr (p == P - 1) {
+                    oa.next();
+                    if constexpr (kFreesB) ob.next();
+                }
+            }
+            constexpr int kWord = k8 ? 0 : q / 2, kByte = (q & 1) * 2;
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+                acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], fa[p % kRing], acc[m][c], wb[kSet][c][kWord],
+                                                   wa[kSet][m][kWord]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        each(position, std::make_integer_sequence<int, P>{});
+    };
+    typedef std::integral_constant<int, 1> one;
+    typedef std::integral_constant<int, 2> two;
+    typedef std::integral_constant<int, 3> three;
+    int macro = 0;
+    for (; macro + 2 <= macros; macro += 2) {
+        step(zero{}, macro);
+        if constexpr (k8) {
+            step(one{}, macro);
+            step(two{}, macro + 1);
+            step(three{}, macro + 1);
+        } else {
+            step(one{}, macro + 1);
+        }
+    }
+    if (macro < macros) {
+        step(zero{}, macro);
+        if constexpr (k8) step(one{}, macro);
+    }
+    wait_for<0, true>();
+}
+
+template <int FORMAT, int BM, int BC, int WM, int WC>
+__global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs a) {
+    typedef MxShape<FORMAT, BM, BC, WM, WC> S;
+    __shared__ __align__(16) unsigned char a0[BM * 128], a1[BM * 128], b0[BC * 128], b1[BC * 128];
+    __shared__ u32x4 ss[4 * S::kScaleRows];
+    unsigned char *const sa[2] = {a0, a1}, *const sb[2] = {b0, b1};
     if (status_at_entry(a.status)) return;
-    const int t = blockIdx.y + gridDim.y * blockIdx.z;
-    if (t >= a.tiles[0]) return;
-    const int e = a.tiles[2 + 2 * t], mt = a.tiles[3 + 2 * t];
+    // Workgroups go round the eight XCDs; each XCD takes a run of tiles of its own,
+    // kGroup columns through an expert's row tiles.
+    const uint32_t cols = (uint32_t)a.cols, tiles = (uint32_t)a.tiles[0];
+    const uint32_t run = (tiles * cols + 7) / 8, at = (blockIdx.x & 7) * run + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= run || at >= tiles * cols) return;
+    const int e = a.tiles[2 + 2 * (at / cols)];
+    const uint32_t f = (uint32_t)a.first[e], n = (uint32_t)a.first[e + 1] - f;
+    uint32_t i = at - f * cols;
+    const uint32_t group = i / (n * kGroup), wide = min(cols - group * kGroup, kGroup);
+    i -= group * n * kGroup;
+    const int mt = (int)(i / wide), ct = (int)(group * kGroup + i % wide);
     const int d = e / a.P, j = e - d * a.P;
     const int64_t row0 = a.offsets[(int64_t)d * (a.P + 1) + j];
     const int64_t M = a.offsets[(int64_t)d * (a.P + 1) + j + 1] - row0;
     const bool glu = a.act == A2AV_ACT_SWIGLU;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, half = lane >> 5;
-    const int64_t m0 = (int64_t)mt * 64 + (wave >> 1) * 32, c0 = (int64_t)blockIdx.x * 128 + (wave & 1) * 64;
-    const int64_t m = m0 + (lane & 31);
-    const bool in_m = m < M;
-    const unsigned char *x = a.x[d] + (row0 + (in_m ? m : 0)) * a.x_stride;
-    const unsigned char *w[2];
-    bool in_c[2];
-#pragma unroll
-    for (int v = 0; v < 2; v++) {
-        const int64_t c = c0 + v * 32 + (lane & 31), n = weight_row(c, a.N, glu);
-        in_c[v] = glu ? n - ((c >> 4) & 1) * a.N < a.N : n < a.N;
-        w[v] = a.weight[d] + ((int64_t)j * a.NW + (in_c[v] ? n : 0)) * a.w_stride;
-    }
-    const int64_t steps = mx_padded(a.K) / 128, x_scales = mx_element_bytes(FORMAT, a.K), w_scales = mx_padded(a.K) / 2;
-    constexpr int kBytes = FORMAT == A2AV_MX_FP8 ? 128 : 64;  // of 128 elements
-    f32x16 acc[2] = {};
-    for (int64_t s = 0; s < steps; s++) {
-        const uint32_t sx = *(const uint32_t *)(x + x_scales + s * 4) >> (half * 8);
-#pragma unroll
-        for (int q = 0; q < 2; q++) {
-            i32x8 fx = {};
-            if constexpr (FORMAT == A2AV_MX_FP8) {
-                // a half wave has elements 16 h .. + 15 and 32 + 16 h .. + 15 of the 64
-                const i32x4 lo = *(const i32x4 *)(x + s * kBytes + q * 64 + half * 16);
-                const i32x4 hi = *(const i32x4 *)(x + s * kBytes + q * 64 + 32 + half * 16);
-                fx = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            } else {
-                const i32x4 lo = *(const i32x4 *)(x + s * kBytes + q * 32 + half * 16);
-                fx = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
-            }
-            if (!in_m) fx = i32x8{};
-#pragma unroll
-            for (int v = 0; v < 2; v++) {
-                i32x4 fw = *(const i32x4 *)(w[v] + s * 64 + q * 32 + half * 16);
-                const uint32_t sw = *(const uint32_t *)(w[v] + w_scales + s * 4) >> (half * 8);
-                if (!in_c[v]) fw = i32x4{};
-                acc[v] = mfma32<FORMAT>(fw, fx, acc[v], in_c[v] ? (int)(sw >> q * 16) & 255 : 0,
-                                        in_m ? (int)(sx >> q * 16) & 255 : 0);
-            }
+    const int64_t m0 = (int64_t)mt * BM, c0 = (int64_t)ct * BC, left = M - m0;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WC, wc = wave % WC;
+    const int64_t padded = mx_padded(a.K), x_bytes = mx_element_bytes(FORMAT, a.K), n0 = glu ? c0 / 2 : c0;
+    const unsigned char *x = a.x[d] + (row0 + m0) * a.x_stride, *w = a.weight[d] + (int64_t)j * a.NW * a.w_stride;
+    typename S::A oa;
+    typename S::B ob;
+    oa.init(x, nullptr, a.x_stride, left, x_bytes, wave, lane);
+    ob.init(w + n0 * a.w_stride, glu ? w + (a.N + n0) * a.w_stride : nullptr, a.w_stride, a.N - n0, padded / 2, wave, lane);
+    MxScales<S> os;
+    {
+        // a row outside has elements 0: any scale that is not NaN will do, and what a
+        // NaN would make of it is not written
+        const int t = threadIdx.x;
+        if (t < BM) {
+            os.row = x + (t < left ? t : 0) * a.x_stride + x_bytes;
+            os.last = (int)(a.x_stride - x_bytes) - 16;
+        } else {
+            const int64_t c = weight_row(c0 + (t < S::kScaleRows ? t - BM : 0), a.N, glu);
+            os.row = w + (c < a.NW ? c : 0) * a.w_stride + padded / 2;
+            os.last = (int)(a.w_stride - padded / 2) - 16;
         }
     }
+    f32x16 acc[S::kBlocksM][2] = {};
+    const int macros = (int)(padded / kMxPad);
+    if (S::kBlocksM >= 4 && left <= WM * 32)
+        mx_contract<FORMAT, BM, BC, WM, WC, 1>(oa, ob, os, sa, sb, ss, macros, acc);
+    else if (S::kBlocksM >= 2 && left <= WM * 32 * (S::kBlocksM / 2))
+        mx_contract<FORMAT, BM, BC, WM, WC, (S::kBlocksM >= 2 ? S::kBlocksM / 2 : 1)>(oa, ob, os, sa, sb, ss, macros, acc);
+    else
+        mx_contract<FORMAT, BM, BC, WM, WC, S::kBlocksM>(oa, ob, os, sa, sb, ss, macros, acc);
+    __syncthreads();
+    // in passes of kPass row blocks, each wave in its own part of the stages
+    constexpr int kPass = S::kBlocksM < 2 ? 1 : 2, kPart = kPass * 32 * 64 * 16 / 4, kParts = S::kWaves / 4;
+    static_assert(kParts * kPart <= BM * 128 && kParts * kPart <= BC * 128, "");
+    const int in = wave / kParts;
+    f32x4 *sums = (f32x4 *)((in == 0 ? a0 : in == 1 ? a1 : in == 2 ? b0 : b1) + wave % kParts * kPart);
 #pragma unroll
-    for (int v = 0; v < 2; v++) put_sums<64>(sums[wave], 0, v, acc[v], lane);
-    asm volatile("" ::: "memory");
-    emit<32, 64>(a, sums[wave], d, j, row0, M, c0, lane, [&](int r) { return m0 + r; });
+    for (int p = 0; p < S::kBlocksM / kPass; p++) {
+        if (p * kPass * WM * 32 >= left) break;
+#pragma unroll
+        for (int u = 0; u < kPass; u++)
+#pragma unroll
+            for (int v = 0; v < 2; v++) put_sums<64>(sums, u, v, acc[p * kPass + u][v], lane);
+        asm volatile("" ::: "memory");
+        emit<kPass * 32, 64>(a, sums, d, j, row0, M, c0 + wc * 64, lane,
+                             [&](int r) { return m0 + ((p * kPass + (r >> 5)) * WM + wm) * 32 + (r & 31); });
+        asm volatile("" ::: "memory");
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -203,6 +461,29 @@ __global__ __launch_bounds__(256) void k_mx_plain(const MxExpertArgs a) {
 static int64_t product_columns(const MxExpertArgs &a) {
     const int64_t n = a.out_type == kOutMx ? mx_padded(a.N) : a.N;
     return a.act == A2AV_ACT_SWIGLU ? (n + 15) / 16 * 32 : n;
+}
+
+// Tile shapes, largest first.
+enum { kBig, kMid, kSmall };
+constexpr int kRows[] = {256, 128, 64}, kCols[] = {256, 128, 128};
+
+// The largest tile of which the product has enough to fill the compute units: R
+// rows over n experts, C product columns.
+static int shape_of(int64_t R, int64_t n, int64_t C) {
+    for (int s = kBig; s < kSmall; s++) {
+        const int64_t t = kRows[s], cols = (C + kCols[s] - 1) / kCols[s];
+        const int64_t tiles = R <= n ? R : R / t + (R % (n * t) ? n / 2 : 0);
+        if (tiles * cols >= 200) return s;
+    }
+    return kSmall;
+}
+
+template <int FORMAT>
+static void launch_tile(const MxExpertArgs &a, int shape, int64_t tiles, hipStream_t stream) {
+    const dim3 g((unsigned)((tiles * a.cols + 7) / 8 * 8));
+    if (shape == kBig) hipLaunchKernelGGL((k_mx_tile<FORMAT, 256, 256, 2, 4>), g, dim3(512), 0, stream, a);
+    else if (shape == kMid) hipLaunchKernelGGL((k_mx_tile<FORMAT, 128, 128, 2, 2>), g, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_mx_tile<FORMAT, 64, 128, 2, 2>), g, dim3(256), 0, stream, a);
 }
 
 }  // namespace a2av
@@ -256,11 +537,17 @@ A2AV_API int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_form
     a.status = status;
     a.W = W;
     a.P = P;
-    launch_plan(W, P, x_rows, expert_offsets, 64, (unsigned char *)workspace, l, status, stream);
-    const int64_t tiles = most_tiles(x_rows, W, P, 64), y = tiles < 32768 ? tiles : 32768;
-    a.cols = (int)((product_columns(a) + 127) / 128);
-    const dim3 g((unsigned)a.cols, (unsigned)y, (unsigned)((tiles + y - 1) / y));
-    if (x_format == A2AV_MX_FP8) hipLaunchKernelGGL(k_mx_plain<A2AV_MX_FP8>, g, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(k_mx_plain<A2AV_MX_FP4>, g, dim3(256), 0, stream, a);
+    int64_t R = 0;
+    for (int d = 0; d < W; d++) R += x_rows[d];
+    int shape = shape_of(R, (int64_t)W * P, product_columns(a));
+    const auto tiles_of = [&](int s) { return most_tiles(x_rows, W, P, kRows[s]); };
+    const auto cols_of = [&](int s) { return (product_columns(a) + kCols[s] - 1) / kCols[s]; };
+    while (shape > kBig && tiles_of(shape) * cols_of(shape) > kMostGroups) shape--;
+    const int64_t tiles = tiles_of(shape);
+    a.cols = (int)cols_of(shape);
+    if (tiles * a.cols > kMostGroups) return A2AV_EARG;
+    launch_plan(W, P, x_rows, expert_offsets, kRows[shape], (unsigned char *)workspace, l, status, stream);
+    if (x_format == A2AV_MX_FP8) launch_tile<A2AV_MX_FP8>(a, shape, tiles, stream);
+    else launch_tile<A2AV_MX_FP4>(a, shape, tiles, stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

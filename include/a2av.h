@@ -865,7 +865,8 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  *                   on failure
  * Arrays that are written overlap no others (out at the base of x: A2AV_EARG).
  * Two kernels: the plan of moe_expert_linear, and the products on matrix cores;
- * their tiles are chosen for as many rows as x_rows allows.
+ * their tiles are chosen for as many rows as x_rows allows (more than 2^22 of
+ * 256 x 256 that x_rows and the experts could need: A2AV_EARG).
  */
 int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_format, int act,
                          const void *const *x, const int64_t *x_rows,

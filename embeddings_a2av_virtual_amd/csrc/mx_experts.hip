@@ -58,8 +58,9 @@ __device__ __forceinline__ Split split(i32x8 v) {
     Split s;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const uint32_t m = ((uint32_t)v[i] >> 6) & 0x01010101u;
-        s.hi[i] = (int)((uint32_t)v[i] & ((m << 8) - m));
+        // a byte permutation gives 0xFF for a selector above 12 and 0 for 12
+        const uint32_t top = ((uint32_t)v[i] & 0x40404040u) | 0x0C0C0C0Cu;
+        s.hi[i] = (int)((uint32_t)v[i] & __builtin_amdgcn_perm(0u, 0u, top));
         s.lo[i] = v[i] ^ s.hi[i];
     }
     return s;
@@ -99,8 +100,8 @@ __device__ __forceinline__ void put_out(const MxExpertArgs &a, int d, int64_t ro
     }
     uint16_t *out = (uint16_t *)a.out[d] + row * a.N + n;
     if (a.wide) {
-        if (a.out_type == kOutBf16) put8<Bf16>(out, y);
-        else put8<Fp16>(out, y);
+        if (a.out_type == kOutBf16) put8<Bf16, true>(out, y);
+        else put8<Fp16, true>(out, y);
         return;
     }
 #pragma unroll
@@ -115,13 +116,17 @@ __device__ __forceinline__ void add_bias(const MxExpertArgs &a, const float *bia
 }
 
 // The rows of a pass; `row_of(r)` is the expert's row behind LDS row r, c0 the
-// first product column of the wave.
-template <int ROWS, int COLS, typename RowOf>
-__device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, int d, int j, int64_t row0, int64_t M,
-                                     int64_t c0, int lane, RowOf row_of) {
-    const bool glu = a.act == A2AV_ACT_SWIGLU;
-    const int per = glu ? COLS / 16 : COLS / 8;  // lanes a row
+// first product column of the wave. Several rows' LDS reads are in flight at once.
+template <int ROWS, int COLS, bool GLU, typename RowOf>
+__device__ __forceinline__ void emit_rows(const MxExpertArgs &a, const f32x4 *sums, int d, int j, int64_t row0, int64_t M,
+                                          int64_t c0, int lane, RowOf row_of) {
+    constexpr int kPer = GLU ? COLS / 16 : COLS / 8, kStep = kWave / kPer;  // lanes a row, rows at once
+    constexpr int kTimes = (ROWS + kStep - 1) / kStep, kMost = GLU ? 2 : 4, kBatch = kTimes < kMost ? kTimes : kMost;
+    static_assert(kTimes % kBatch == 0, "");
     const int64_t end = a.out_type == kOutMx ? mx_padded(a.N) : a.N;
+    const int q = lane % kPer;
+    const int64_t n = (GLU ? c0 / 2 : c0) + q * 8;
+    if (n >= end) return;
     const float *bias = a.bias[d] + (int64_t)j * a.NW;
     const auto take = [&](int r, int at, float(&y)[8]) {
         const f32x4 lo = sums[chunk<COLS>(r, at)], hi = sums[chunk<COLS>(r, at + 1)];
@@ -131,28 +136,38 @@ __device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, i
             y[i + 4] = hi[i];
         }
     };
-    for (int r = lane / per; r < ROWS; r += kWave / per) {
-        const int64_t m = row_of(r);
-        if (m >= M) continue;
-        const int q = lane % per;
-        const int64_t n = (glu ? c0 / 2 : c0) + q * 8;
-        if (n >= end) continue;
-        float y[8];
-        // gated: blocks of 16 gate and 16 up columns alternate
-        take(r, glu ? (q >> 1) * 8 + (q & 1) * 2 : q * 2, y);
-        if (a.has_bias) add_bias(a, bias, n, y);
-        if (glu) {
-            float up[8];
-            take(r, (q >> 1) * 8 + (q & 1) * 2 + 4, up);
-            if (a.has_bias) add_bias(a, bias + a.N, n, up);
+    // gated: blocks of 16 gate and 16 up columns alternate
+    const int at = GLU ? (q >> 1) * 8 + (q & 1) * 2 : q * 2;
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = y[i] * sigmoid(y[i]) * up[i];
-        } else if (a.act != A2AV_ACT_NONE) {
+    for (int r0 = 0; r0 < kTimes * kStep; r0 += kBatch * kStep) {
+        float y[kBatch][8], up[GLU ? kBatch : 1][8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = act_of(a.act, y[i]);
+        for (int b = 0; b < kBatch; b++) {
+            take(r0 + b * kStep + lane / kPer, at, y[b]);
+            if constexpr (GLU) take(r0 + b * kStep + lane / kPer, at + 4, up[b]);
         }
-        put_out(a, d, row0 + m, n, y);
+#pragma unroll
+        for (int b = 0; b < kBatch; b++) {
+            const int64_t m = row_of(r0 + b * kStep + lane / kPer);
+            if (m >= M) continue;
+            if (a.has_bias) add_bias(a, bias, n, y[b]);
+            if constexpr (GLU) {
+                if (a.has_bias) add_bias(a, bias + a.N, n, up[b]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) y[b][i] = y[b][i] * sigmoid(y[b][i]) * up[b][i];
+            } else if (a.act != A2AV_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) y[b][i] = act_of(a.act, y[b][i]);
+            }
+            put_out(a, d, row0 + m, n, y[b]);
+        }
     }
+}
+template <int ROWS, int COLS, typename RowOf>
+__device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, int d, int j, int64_t row0, int64_t M,
+                                     int64_t c0, int lane, RowOf row_of) {
+    if (a.act == A2AV_ACT_SWIGLU) emit_rows<ROWS, COLS, true>(a, sums, d, j, row0, M, c0, lane, row_of);
+    else emit_rows<ROWS, COLS, false>(a, sums, d, j, row0, M, c0, lane, row_of);
 }
 
 // ------------------------------------------------------------------ the tiles
@@ -206,30 +221,31 @@ struct MxShape {
     static constexpr int kBlocksM = BM / WM / 32, kBlocksC = BC / WC / 32;
     static constexpr int kQuarters = FORMAT == A2AV_MX_FP8 ? 2 : 4;  // of 64 elements in a step
     static constexpr int kScaleRows = BM + BC;
-    static_assert(kScaleRows <= kThreads && kBlocksC == 2, "");
+    static_assert(BM <= kThreads / 2 && BC <= kThreads / 2 && kBlocksC == 2, "");
     typedef MxOperand<BM, kWaves> A;
     typedef MxOperand<BC, kWaves> B;
 };
 
-// The scales of a tile's rows, 1024 elements (32 bytes a row) at a time: one row of
-// x or of the weight per thread, through registers to the two LDS buffers. In LDS
-// the halves of 16 bytes lie apart, row after row.
+// The scales of a tile's rows, 1024 elements (32 bytes a row) at a time: half of a
+// row's, of x and of the weight, per thread, through registers to the two LDS
+// buffers. In LDS the halves of 16 bytes lie apart, row after row.
 constexpr int kScaleMacros = 4;  // steps of 256 elements in a buffer
 
-template <typename S>
+template <int BM, int BC>
 struct MxScales {
-    const unsigned char *row;  // the thread's row's scales
-    int last;                  // offset of the last 16 bytes inside the row
+    const unsigned char *x, *w;  // the thread's rows' scales
+    int last_x, last_w;          // offset of the last 16 bytes inside the rows
     u32x4 v[2];
     __device__ __forceinline__ void load(int chunk) {
-        v[0] = *(const u32x4 *)(row + min(chunk * 32, last));
-        v[1] = *(const u32x4 *)(row + min(chunk * 32 + 16, last));
+        const int at = chunk * 32 + (threadIdx.x & 1) * 16;
+        v[0] = *(const u32x4 *)(x + min(at, last_x));
+        v[1] = *(const u32x4 *)(w + min(at, last_w));
     }
     __device__ __forceinline__ void store(u32x4 *lds, int chunk) const {
-        if ((int)threadIdx.x >= S::kScaleRows) return;
-        lds += (chunk & 1) * 2 * S::kScaleRows + threadIdx.x;
-        lds[0] = v[0];
-        lds[S::kScaleRows] = v[1];
+        const int row = threadIdx.x / 2;
+        lds += ((chunk & 1) * 2 + (threadIdx.x & 1)) * (BM + BC) + row;
+        if (row < BM) lds[0] = v[0];
+        if (row < BC) lds[BM] = v[1];
     }
 };
 
@@ -269,13 +285,16 @@ __device__ __forceinline__ void each(const F &f, std::integer_sequence<int, I...
 template <int FORMAT, bool SPLIT, int BM, int BC, int WM, int WC, int NB>
 __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM, WC>::A &oa,
                                             typename MxShape<FORMAT, BM, BC, WM, WC>::B &ob,
-                                            MxScales<MxShape<FORMAT, BM, BC, WM, WC>> &os, unsigned char *const (&sa)[2],
+                                            MxScales<BM, BC> &os, unsigned char *const (&sa)[2],
                                             unsigned char *const (&sb)[2], u32x4 *ss, int macros,
                                             f32x16 (&acc)[MxShape<FORMAT, BM, BC, WM, WC>::kBlocksM][2]) {
     typedef MxShape<FORMAT, BM, BC, WM, WC> S;
     typedef typename MxFrag<FORMAT>::type frag;
     constexpr bool k8 = FORMAT == A2AV_MX_FP8;
-    constexpr int Q = S::kQuarters, P = Q * NB, kRing = NB >= 4 ? 4 : 2, kAhead = kRing - 1;
+    // where rows are split, that is done a position ahead, beside the matrix
+    // instructions of the one before
+    constexpr bool kPipe = SPLIT && NB >= 2;
+    constexpr int Q = S::kQuarters, P = Q * NB, kRing = NB >= 4 && !kPipe ? 4 : 2, kAhead = kPipe ? 2 : kRing - 1;
     constexpr int kLoadsA = (NB * WM * 32 + S::kWaves * 8 - 1) / (S::kWaves * 8) < S::A::kLoads
                                 ? (NB * WM * 32 + S::kWaves * 8 - 1) / (S::kWaves * 8) : S::A::kLoads;
     constexpr int kLoadsB = S::B::kLoads;
@@ -343,6 +362,8 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
     read_b(fb[0], sb[0], 0);
 #pragma unroll
     for (int p = 0; p < kAhead; p++) fa[p] = read_a(sa[0], p % NB, p / NB);
+    Split parts[2];
+    if constexpr (kPipe) parts[0] = split(fa[0]);
     // step `i` of the unrolled ones (its stages by its number), in macro step `macro`
     const auto step = [&](auto number, int macro) __attribute__((always_inline)) {
         constexpr int i = decltype(number)::value;
@@ -358,7 +379,8 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
         const auto position = [&](auto place) __attribute__((always_inline)) {
             constexpr int p = decltype(place)::value, q = p / NB, m = p % NB, next = p + kAhead;
             if constexpr (p == P - kAhead) {
-                wait_for<0, true>();
+                // the weights behind the rows of the step before have one more to arrive
+                wait_for<k8 && !kFreesB ? kLoadsB : 0, true>();
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -369,9 +391,12 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
             if constexpr (p == 0)
                 read_scales(std::integral_constant<int, 1 - kSet>{}, kFreesB ? macro + 1 : macro, k8 && !kFreesB ? 1 : 0);
             if constexpr (p >= P - kAhead) {
+                // all loads of the rows, then those of the weights
                 constexpr int k = p - (P - kAhead);
-                oa.template load<kLoadsA * k / kAhead, kLoadsA *(k + 1) / kAhead>(sa[kStageA], wave);
-                if constexpr (kFreesB) ob.template load<kLoadsB * k / kAhead, kLoadsB *(k + 1) / kAhead>(sb[kStageB], wave);
+                constexpr int kAll = kLoadsA + (kFreesB ? kLoadsB : 0), kFrom = kAll * k / kAhead, kTo = kAll * (k + 1) / kAhead;
+                oa.template load<(kFrom < kLoadsA ? kFrom : kLoadsA), (kTo < kLoadsA ? kTo : kLoadsA)>(sa[kStageA], wave);
+                if constexpr (kTo > kLoadsA)
+                    ob.template load<(kFrom > kLoadsA ? kFrom - kLoadsA : 0), kTo - kLoadsA>(sb[kStageB], wave);
                 if constexpr (p == P - 1) {
                     oa.next();
                     if constexpr (kFreesB) ob.next();
@@ -379,7 +404,8 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
             }
             constexpr int kWord = k8 ? 0 : q / 2, kByte = (q & 1) * 2;
             if constexpr (SPLIT) {
-                const Split x = split(fa[p % kRing]);
+                if constexpr (!kPipe) parts[p & 1] = split(fa[p % kRing]);
+                const Split &x = parts[p & 1];
 #pragma unroll
                 for (int c = 0; c < 2; c++)
                     acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], x.hi, acc[m][c], wb[kSet][c][kWord],
@@ -393,6 +419,15 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
                 for (int c = 0; c < 2; c++)
                     acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], fa[p % kRing], acc[m][c], wb[kSet][c][kWord],
                                                        wa[kSet][m][kWord]);
+            }
+            if constexpr (kPipe) {
+                parts[(p + 1) & 1] = split(fa[(p + 1) % kRing]);
+                // a quarter of the splitting behind each matrix instruction
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -451,19 +486,16 @@ __global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs
     typename S::B ob;
     oa.init(x, nullptr, a.x_stride, left, x_bytes, wave, lane);
     ob.init(w + n0 * a.w_stride, glu ? w + (a.N + n0) * a.w_stride : nullptr, a.w_stride, a.N - n0, padded / 2, wave, lane);
-    MxScales<S> os;
+    MxScales<BM, BC> os;
     {
         // a row outside has elements 0: any scale that is not NaN will do, and what a
         // NaN would make of it is not written
-        const int t = threadIdx.x;
-        if (t < BM) {
-            os.row = x + (t < left ? t : 0) * a.x_stride + x_bytes;
-            os.last = (int)(a.x_stride - x_bytes) - 16;
-        } else {
-            const int64_t c = weight_row(c0 + (t < S::kScaleRows ? t - BM : 0), a.N, glu);
-            os.row = w + (c < a.NW ? c : 0) * a.w_stride + padded / 2;
-            os.last = (int)(a.w_stride - padded / 2) - 16;
-        }
+        const int r = threadIdx.x / 2;
+        const int64_t c = weight_row(c0 + (r < BC ? r : 0), a.N, glu);
+        os.x = x + (r < BM && r < left ? r : 0) * a.x_stride + x_bytes;
+        os.w = w + (c < a.NW ? c : 0) * a.w_stride + padded / 2;
+        os.last_x = (int)(a.x_stride - x_bytes) - 16;
+        os.last_w = (int)(a.w_stride - padded / 2) - 16;
     }
     f32x16 acc[S::kBlocksM][2] = {};
     const int macros = (int)(padded / kMxPad);
@@ -685,7 +717,7 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
     }
     __syncthreads();
     if (wave != 0) return;
-    emit<kFewRows, kCols>(a, sums[0], d, j, row0, rows, (int64_t)ct * kCols, lane, [](int r) { return (int64_t)r; });
+    emit_rows<kFewRows, kCols, GLU>(a, sums[0], d, j, row0, rows, (int64_t)ct * kCols, lane, [](int r) { return (int64_t)r; });
 }
 
 // ------------------------------------------------------------------ host

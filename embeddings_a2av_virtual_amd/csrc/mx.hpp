@@ -87,52 +87,92 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
     return b > m ? b : m;
 }
 
-// The scale byte of a block whose largest magnitude has these bits, and the
-// elements of a lane's eight values; every lane of the quad is active. A block
-// with an infinity or NaN is NaN: its scale says so and its elements are 0.
-template <int FORMAT>
-__device__ __forceinline__ typename Mx<FORMAT>::packed mx_block(const float (&v)[8], int &scale) {
+// The bits of the largest magnitude of a quad's values, NaN above all.
+__device__ __forceinline__ uint32_t quad_top(const float (&v)[8]) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFFu;
         m = u > m ? u : m;
     }
-    const int e = (int)(quad_max(m) >> 23);
+    return quad_max(m);
+}
+
+// The same where no value is NaN.
+__device__ __forceinline__ uint32_t quad_largest(const float (&v)[8]) {
+    float m;
+    asm("v_max3_f32 %0, |%1|, |%2|, 0" : "=v"(m) : "v"(v[0]), "v"(v[1]));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(v[i]), "v"(v[i + 1]));
+    return quad_max(__float_as_uint(m));
+}
+
+// The scale byte of a block whose largest magnitude has these bits, and the
+// elements of a lane's eight values; every lane of the quad is active. A block
+// with an infinity or NaN is NaN: its scale says so and its elements are 0.
+template <int FORMAT>
+__device__ __forceinline__ typename Mx<FORMAT>::packed mx_block(const float (&v)[8], int &scale) {
+    const int e = (int)(quad_top(v) >> 23);
     const bool bad = e == 255;
     scale = bad ? kMxNan : e > Mx<FORMAT>::kTop ? e - Mx<FORMAT>::kTop : 0;
     // 2^(127 - scale): the product is exact, or far below the smallest element
     const float inv = bad ? 0.0f : __uint_as_float((uint32_t)(254 - scale) << 23);
     float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) s[i] = bad ? 0.0f : v[i] * inv;
-    return Mx<FORMAT>::pack(s);
+    for (int i = 0; i < 8; i++) s[i] = v[i] * inv;
+    return bad ? typename Mx<FORMAT>::packed{} : Mx<FORMAT>::pack(s);
 }
 
-// The same of values in double, from whose last places the elements of a norm
-// are decided: values next to the middle of two elements are not rounded to
-// fp32 in between, which could put them there. What an element depends on is
-// the value's upper word (20 bits of its mantissa) and whether bits follow.
+// The scale byte for a largest magnitude in double, and the factor 2^(127 - it);
+// NaN or an infinity gives the byte of NaN.
+template <int FORMAT>
+__device__ __forceinline__ int mx_scale_of(uint32_t upper, double &inv) {
+    const int e = (int)((upper & 0x7FFFFFFFu) >> 20), want = e - 1023 + 127 - Mx<FORMAT>::kTop;
+    const int scale = want < 0 ? 0 : want > 254 ? 254 : want;
+    inv = __longlong_as_double((int64_t)(1023 + 127 - scale) << 52);
+    return e == 2047 ? kMxNan : scale;
+}
+__device__ __forceinline__ uint32_t upper_word(double v) { return (uint32_t)((uint64_t)__double_as_longlong(v) >> 32); }
+
+// A double for the rounding to an element: its upper word (20 bits of the mantissa)
+// with the last bit set if any bits follow is on the same side of every middle of
+// two elements as the double, and exact in fp32. A rounding to fp32 could put it on
+// a middle.
+__device__ __forceinline__ float jam(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t rest = (uint32_t)u < 1u ? (uint32_t)u : 1u;
+    return (float)__longlong_as_double((int64_t)((uint64_t)((uint32_t)(u >> 32) | rest) << 32));
+}
+
+// The same for values in double, from whose last places the elements of a norm are
+// decided.
 template <int FORMAT>
 __device__ __forceinline__ typename Mx<FORMAT>::packed mx_block(const double (&v)[8], int &scale) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const uint32_t u = (uint32_t)(__double_as_longlong(v[i]) >> 32) & 0x7FFFFFFFu;
+        const uint32_t u = upper_word(v[i]) & 0x7FFFFFFFu;
         m = u > m ? u : m;
     }
-    const int e = (int)(quad_max(m) >> 20);
-    const bool bad = e == 2047;
-    const int want = e - 1023 + 127 - Mx<FORMAT>::kTop;
-    scale = bad ? kMxNan : want < 0 ? 0 : want > 254 ? 254 : want;
-    const double inv = bad ? 0.0 : __longlong_as_double((int64_t)(1023 + 127 - scale) << 52);
+    double inv;
+    scale = mx_scale_of<FORMAT>(quad_max(m), inv);
     float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint64_t u = (uint64_t)__double_as_longlong(bad ? 0.0 : v[i] * inv);
-        s[i] = (float)__longlong_as_double((int64_t)((u & 0xFFFFFFFF00000000ull) | ((uint32_t)u ? 1ull << 32 : 0)));
-    }
-    return Mx<FORMAT>::pack(s);
+    for (int i = 0; i < 8; i++) s[i] = jam(v[i] * inv);
+    return scale == kMxNan ? typename Mx<FORMAT>::packed{} : Mx<FORMAT>::pack(s);
+}
+
+// The same for the products v[i] * r, r in double, of a quad whose largest v has the
+// magnitude m: one product in double each.
+template <int FORMAT>
+__device__ __forceinline__ typename Mx<FORMAT>::packed mx_block(const float (&v)[8], uint32_t m, double r, int &scale) {
+    double inv;
+    scale = mx_scale_of<FORMAT>(upper_word((double)__uint_as_float(m) * r), inv);
+    inv *= r;
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) s[i] = jam((double)v[i] * inv);
+    return scale == kMxNan ? typename Mx<FORMAT>::packed{} : Mx<FORMAT>::pack(s);
 }
 
 // 2^(b - 127) as a factor: 2^-127 is subnormal, 255 is NaN.

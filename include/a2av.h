@@ -775,7 +775,8 @@ int moe_mx_dequantize(int W, int64_t H, int type, int format, const void *const 
  *   h = x + residual, in fp32, rounded to type   (residual NULL: h = x)
  *   y = h / sqrt(mean(h^2) + eps) * weight        (in double)
  *   sum = h,  out = y rounded to type,  rows = y as a microscaled row
- * (y is rounded once into either; moe_mx_quantize says how blocks are made).
+ * (moe_mx_quantize says how blocks are made; y is rounded once into rows and
+ * into an out in fp32; an out of 16 bits has two roundings of fp32 before).
  *   H             1 .. A2AV_MAX_WIDTH;  T up to 2^30
  *   type          A2AV_DT_* of x, residual, weight, sum and out
  *   eps           at least 0
@@ -791,8 +792,8 @@ int moe_mx_dequantize(int W, int64_t H, int type, int format, const void *const 
  *   status        only read
  * sum and out may each be x or the residual, but not one array; other arrays
  * that are written overlap no others (rows at the base of any, sum at that of
- * out: A2AV_EARG). One kernel; widths that are multiples of 8 up to 32768 at
- * 16-byte-aligned bases are read once.
+ * out: A2AV_EARG). One kernel; rows of up to 16384 are read once, wider ones
+ * twice.
  */
 int moe_rms_norm(int W, int64_t T, int64_t H, int type, double eps, const void *const *x,
                  const void *const *residual, const void *weight, void *const *sum,

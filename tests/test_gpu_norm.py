@@ -292,3 +292,34 @@ def test_gradient_refusals():
         with pytest.raises((ValueError, B.A2avError, TypeError)):
             B.moe_rms_norm_backward(**{**ok, **kw})
     B.moe_rms_norm_backward(**ok)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H", [1023, 1025, 5003, 8191, 9001, 16383])
+def test_odd_widths(kind, H):
+    """A last vector that the row ends in, for every way that a row is spread over threads."""
+    g = torch.Generator().manual_seed(H)
+    t, W, T = TYPES[kind], 2, 5
+    weight = (1 + 0.2 * torch.randn(H, generator=g)).to(t)
+    hs, gs, ds = (_rows(g, W, T, H, t) for _ in range(3))
+    check(hs, gs, weight, M.FP8, pad=t.itemsize)
+    check(hs, None, weight, M.FP4)
+    check_grad(hs, weight, gs, ds, pad=t.itemsize)
+
+
+@pytest.mark.parametrize("H", [264, 1003, 1032, 5003, 16392])
+@pytest.mark.parametrize("last", [-1.0, float("nan"), float("inf")])
+def test_padding_is_zero_whatever_the_last_weights(H, last):
+    g = torch.Generator().manual_seed(H)
+    weight = torch.randn(H, generator=g)
+    weight[-3:] = last
+    for t in TYPES.values():
+        xs = _rows(g, 1, 3, H, t)
+        for form in (M.FP8, M.FP4):
+            got = norm(xs, None, weight.to(t), form, want_out=False)["rows"][0]
+            n, per = M.padded(H), 1 if form == M.FP8 else 2
+            blocks = -(-H // 32)
+            assert not got[:, -(-H // per):n // per].any(), form
+            assert not got[:, n // per + blocks:n // per + n // 32].any(), form
+            if last != -1.0:
+                assert (got[:, n // per + blocks - 1] == 255).all()

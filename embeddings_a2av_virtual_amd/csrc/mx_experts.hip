@@ -547,9 +547,6 @@ __device__ __forceinline__ f32x4 mfma_few(i32x4 w, i32x8 x, f32x4 c, uint32_t sw
 __device__ __forceinline__ i32x4 load16(rsrc_t b, uint32_t off) {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
 }
-__device__ __forceinline__ u32x4 load16u(rsrc_t b, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
-}
 
 // What the plan finds, for row tile t of kFewRows rows: false if the offsets are
 // wrong (the first workgroup says so), or there are no more tiles. Every thread of
@@ -631,7 +628,7 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
     for (int from = 0; from < macros; from += kFewMacros) {
         const int to = min(from + kFewMacros, macros);
         // the scales of all rows for these steps, sixteen bytes a load, rows along the threads
-        u32x4 sv[kScaleLoads];
+        i32x4 sv[kScaleLoads];
 #pragma unroll
         for (int i = 0; i < kScaleLoads; i++) {
             const int k = i * kThreads + threadIdx.x, row = k / (kFewMacros / 2), at = k % (kFewMacros / 2);
@@ -640,9 +637,9 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
             const int wrow = GLU ? (row >> 5) * 16 + (row & 15) : row;
             const bool in = from + at * 2 < macros;
             if (row < kCols)
-                sv[i] = load16u(GLU && (row & 16) ? bw[1] : bw[0], in ? (uint32_t)wrow * ws + w_scales + byte : kOutside);
+                sv[i] = load16(GLU && (row & 16) ? bw[1] : bw[0], in ? (uint32_t)wrow * ws + w_scales + byte : kOutside);
             else
-                sv[i] = load16u(bx, in ? (uint32_t)(row - kCols) * xs + x_scales + byte : kOutside);
+                sv[i] = load16(bx, in ? (uint32_t)(row - kCols) * xs + x_scales + byte : kOutside);
         }
         bool stored = false;
         for (int macro = from + wave; macro < to || !stored; macro += kFewWaves) {
@@ -671,7 +668,7 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
 #pragma unroll
                 for (int i = 0; i < kScaleLoads; i++) {
                     const int k = i * kThreads + threadIdx.x, r = k / (kFewMacros / 2), at = k % (kFewMacros / 2);
-                    if (r < kScaleRows) *(u32x4 *)(scales + r * kFewScaleRow + at * 16) = sv[i];
+                    if (r < kScaleRows) *(i32x4 *)(scales + r * kFewScaleRow + at * 16) = sv[i];
                 }
                 __syncthreads();
                 stored = true;

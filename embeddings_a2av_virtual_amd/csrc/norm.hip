@@ -641,7 +641,7 @@ A2AV_API int moe_rms_norm_backward(int W, int64_t T, int64_t H, int type, double
     a.rows = (int64_t)W * T;
     a.eps = eps;
     a.per = 1.0 / (double)H;
-    a.groups = (int)grad_shape(W, T, H).groups;
+    a.groups = (int)up_to(grad_shape(W, T, H).groups, max_grid());
     a.has_d_sum = d_sum != nullptr;
     a.has_d_weight = d_weight != nullptr;
     if (T > 0) {

@@ -844,6 +844,9 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  *   h = x[d][row] . weight[d][j]^T + bias[d][j]     (fp32 sums)
  *   out[d][row] = act(h), rounded once
  * with A2AV_ACT_SWIGLU as moe_expert_linear has it (2N weight rows, N outputs).
+ * Eight neighbouring products are summed exactly; but of A2AV_MX_FP8 rows with
+ * an out of 16 bits a sum of eight may drop what lies more than 2^14 below its
+ * largest product (5e-6 of random sums, a thousandth of out's rounding).
  * The products read the elements as they lie: a block that stands for NaN gives
  * NaN where its row or column goes.
  *   K, N            1 .. A2AV_MAX_WIDTH
@@ -867,7 +870,9 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  * Arrays that are written overlap no others (out at the base of x: A2AV_EARG).
  * Two kernels: the plan of moe_expert_linear, and the products on matrix cores;
  * their tiles are chosen for as many rows as x_rows allows (more than 2^22 of
- * 256 x 256 that x_rows and the experts could need: A2AV_EARG).
+ * 256 x 256 that x_rows and the experts could need: A2AV_EARG). Where x_rows
+ * allows at most 12 rows an expert it is one kernel, which reads the offsets
+ * itself.
  */
 int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_format, int act,
                          const void *const *x, const int64_t *x_rows,

@@ -266,3 +266,21 @@ def test_refusals():
     B.moe_expert_linear_mx(**ok)
     torch.cuda.synchronize()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("K", [8192, 8193, 8448, 16384, 20000, 24600])
+def test_long_contractions_of_few_rows(form, K):
+    """More scales of a row than one filling of LDS takes, up to four fillings."""
+    Experts([[3, 0, 16, 1], [0, 2, 0, 17]], K, 40, form, "none", "bf16", _seed(form, K), whole=True).check()
+    Experts([[1, 0], [2, 5]], K, 24, form, "swiglu", "fp8", _seed(form, K)).check()
+
+
+def test_offsets_are_checked_without_rows():
+    e = Experts([[0, 0], [0, 0]], 300, 64, "fp8", "none", "bf16", 22)
+    assert e.forward(x_rows=[0, 0])[0] == 0
+    for at, v, want in (((0, 0), 1, B.ST_BAD_OFFSETS), ((1, 2), 1, B.ST_SEND_OVERRUN), ((1, 1), -1, B.ST_BAD_OFFSETS)):
+        o = e.offsets.clone()
+        o[at] = v
+        st, out = e.forward(offsets=o, x_rows=[0, 0])
+        assert st == want and all((x.view(torch.uint8) == SENT).all() for x in out)

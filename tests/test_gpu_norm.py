@@ -323,3 +323,11 @@ def test_padding_is_zero_whatever_the_last_weights(H, last):
             assert not got[:, n // per + blocks:n // per + n // 32].any(), form
             if last != -1.0:
                 assert (got[:, n // per + blocks - 1] == 255).all()
+
+
+@pytest.mark.parametrize("grid", [1, 5])
+def test_small_grids_of_the_gradient(grid, monkeypatch):
+    monkeypatch.setenv("A2AV_MAX_GRID", str(grid))
+    g = torch.Generator().manual_seed(grid)
+    for H in (264, 1003, 2056, 16392):
+        check_grad(*[torch.ones(H).half() if i == 1 else _rows(g, 2, 9, H, torch.float16) for i in range(4)])

@@ -15,10 +15,10 @@ ROWS, COLS = (256, 128, 64), (256, 128, 128)
 
 
 def tile_of(rows, experts, cols):
-    """The library's choice: the largest tile with enough of them."""
-    for i in range(2):
+    """The library's choice: the largest tile with enough of them that the mean expert half fills."""
+    for i in range(2 if rows <= 64 * experts else 1 if rows <= 128 * experts else 0, 2):
         t = ROWS[i]
-        tiles = rows if rows <= experts else rows // t + (experts // 2 if rows % (experts * t) else 0)
+        tiles = rows // t + (experts // 2 if rows % (experts * t) else 0)
         if tiles * -(-cols // COLS[i]) >= 200:
             return i
     return 2

@@ -8,9 +8,12 @@
 //
 //   k_mx_tile   one tile, operands through LDS
 //   k_mx_few    32 columns of up to 16 rows, which read their weights once
+//
+// Outputs of 8 bits (MX) come out as in 64 bits wherever fp32 can hold the sums.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
+#include <type_traits>
 #include <utility>
 
 #include "experts.hpp"
@@ -50,7 +53,8 @@ struct MxExpertArgs {
 // element of 8 bits it decides three in ten thousand of them otherwise than fp32
 // sums. There an e4m3 operand is split by its exponent's top bit into elements of 2
 // and above and those below; neither part's products with e2m1 span 2^14, so both
-// sums of eight are exact.
+// sums of eight are exact, and with a sum in fp32 for either part, both of few bits,
+// so are most of these (added in double at the end).
 struct Split {
     i32x8 hi, lo;
 };
@@ -84,20 +88,74 @@ __device__ __forceinline__ void put_sums(f32x4 *sums, int u, int v, const f32x16
             f32x4{acc[g * 4], acc[g * 4 + 1], acc[g * 4 + 2], acc[g * 4 + 3]};
 }
 
+// Activations where the output becomes an element of 8 bits, in double to 1e-10: the
+// fp32 ones are a few steps off, which decides an element near a border otherwise than
+// the formula (K 7168, SwiGLU: 59 of 33 million elements with one fp32 sum and these
+// in fp32, 42 with these in double, 1 with the two sums of the split as well; 8 experts
+// of 512 rows).
+__device__ __forceinline__ double exp_wide(double x) {
+    const double t = __builtin_fmin(__builtin_fmax(x * 1.4426950408889634, -1000.0), 1000.0), n = __builtin_rint(t);
+    const double f = (t - n) * 0.69314718055994531;  // at most 0.35: the series to f^9 leaves 1e-11
+    double p = 1.0 / 362880;
+    p = __builtin_fma(p, f, 1.0 / 40320);
+    p = __builtin_fma(p, f, 1.0 / 5040);
+    p = __builtin_fma(p, f, 1.0 / 720);
+    p = __builtin_fma(p, f, 1.0 / 120);
+    p = __builtin_fma(p, f, 1.0 / 24);
+    p = __builtin_fma(p, f, 1.0 / 6);
+    p = __builtin_fma(p, f, 0.5);
+    p = __builtin_fma(p, f, 1.0);
+    p = __builtin_fma(p, f, 1.0);
+    return p * __longlong_as_double((int64_t)((int)n + 1023) << 52);
+}
+__device__ __forceinline__ double inverse(double d) {  // of 1 .. 2^1001
+    const double r = __builtin_amdgcn_rcp(d), e = __builtin_fma(-d, r, 1.0);
+    return __builtin_fma(r, __builtin_fma(e, e, e), r);
+}
+__device__ __forceinline__ double silu_wide(double h) { return h * inverse(1.0 + exp_wide(-h)); }
+
+// As normal_cdf, a polynomial in t - 0.6 to 5e-11 for |h| <= 19.
+__device__ __forceinline__ double gelu_wide(double h) {
+    const double x = __builtin_fabs(h) * 0.70710678118654752, t = inverse(1.0 + 0.3 * x), u = t - 0.6;
+    double p = -0.021166241996014044;
+    p = __builtin_fma(p, u, 0.0105805190538479);
+    p = __builtin_fma(p, u, 0.063256953723092021);
+    p = __builtin_fma(p, u, -0.0021860954671192008);
+    p = __builtin_fma(p, u, -0.15132855689646429);
+    p = __builtin_fma(p, u, -0.1364120761610744);
+    p = __builtin_fma(p, u, 0.22425531289121886);
+    p = __builtin_fma(p, u, 0.80774900059842292);
+    p = __builtin_fma(p, u, 1.2778910601161468);
+    p = __builtin_fma(p, u, 1.3850097074199901);
+    p = __builtin_fma(p, u, 1.1416704294489632);
+    p = __builtin_fma(p, u, 0.74455288756601934);
+    p = __builtin_fma(p, u, 0.38928356801009617);
+    const double q = 0.5 * p * t * exp_wide(-0.5 * h * h);
+    return h * (h > 0.0 ? 1.0 - q : q);
+}
+__device__ __forceinline__ double act_wide(int act, double h) {
+    switch (act) {
+    case A2AV_ACT_RELU: return h < 0.0 ? 0.0 : h;
+    case A2AV_ACT_GELU: return gelu_wide(h);
+    case A2AV_ACT_SILU: return silu_wide(h);
+    default: return h;
+    }
+}
+
 // Eight outputs y of row `row`, columns n .. n + 7; every lane of a quad comes
 // here together with the same row and its own eight columns of a block of 32.
-__device__ __forceinline__ void put_out(const MxExpertArgs &a, int d, int64_t row, int64_t n, float (&y)[8]) {
-    if (a.out_type == kOutMx) {
+__device__ __forceinline__ void put_mx(const MxExpertArgs &a, int d, int64_t row, int64_t n, double (&y)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (n + i >= a.N) y[i] = 0.0f;
-        int scale;
-        const auto e = mx_block<A2AV_MX_FP8>(y, scale);
-        unsigned char *out = (unsigned char *)a.out[d] + row * a.out_stride;
-        *(u32x2 *)(out + n) = e;
-        if (n % kMxBlock == 0) out[mx_padded(a.N) + n / kMxBlock] = (unsigned char)scale;
-        return;
-    }
+    for (int i = 0; i < 8; i++)
+        if (n + i >= a.N) y[i] = 0.0;
+    int scale;
+    const auto e = mx_block<A2AV_MX_FP8>(y, scale);
+    unsigned char *out = (unsigned char *)a.out[d] + row * a.out_stride;
+    *(u32x2 *)(out + n) = e;
+    if (n % kMxBlock == 0) out[mx_padded(a.N) + n / kMxBlock] = (unsigned char)scale;
+}
+
+__device__ __forceinline__ void put_out(const MxExpertArgs &a, int d, int64_t row, int64_t n, const float (&y)[8]) {
     uint16_t *out = (uint16_t *)a.out[d] + row * a.N + n;
     if (a.wide) {
         if (a.out_type == kOutBf16) put8<Bf16, true>(out, y);
@@ -109,7 +167,8 @@ __device__ __forceinline__ void put_out(const MxExpertArgs &a, int d, int64_t ro
         if (n + i < a.N) out[i] = a.out_type == kOutBf16 ? Bf16::from_float(y[i]) : Fp16::from_float(y[i]);
 }
 
-__device__ __forceinline__ void add_bias(const MxExpertArgs &a, const float *bias, int64_t n, float (&y)[8]) {
+template <typename T>
+__device__ __forceinline__ void add_bias(const MxExpertArgs &a, const float *bias, int64_t n, T (&y)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i++)
         if (a.wide || n + i < a.N) y[i] += bias[n + i];
@@ -117,30 +176,34 @@ __device__ __forceinline__ void add_bias(const MxExpertArgs &a, const float *bia
 
 // The rows of a pass; `row_of(r)` is the expert's row behind LDS row r, c0 the
 // first product column of the wave. Several rows' LDS reads are in flight at once.
-template <int ROWS, int COLS, bool GLU, typename RowOf>
-__device__ __forceinline__ void emit_rows(const MxExpertArgs &a, const f32x4 *sums, int d, int j, int64_t row0, int64_t M,
-                                          int64_t c0, int lane, RowOf row_of) {
+// MX: the outputs are microscaled; TWO: the sums are sums + low.
+template <int ROWS, int COLS, bool GLU, bool MX, bool TWO, typename RowOf>
+__device__ __forceinline__ void emit_rows(const MxExpertArgs &a, const f32x4 *sums, const f32x4 *low, int d, int j,
+                                          int64_t row0, int64_t M, int64_t c0, int lane, RowOf row_of) {
     constexpr int kPer = GLU ? COLS / 16 : COLS / 8, kStep = kWave / kPer;  // lanes a row, rows at once
-    constexpr int kTimes = (ROWS + kStep - 1) / kStep, kMost = GLU ? 2 : 4, kBatch = kTimes < kMost ? kTimes : kMost;
+    constexpr int kTimes = (ROWS + kStep - 1) / kStep, kMost = GLU || MX ? 2 : 4, kBatch = kTimes < kMost ? kTimes : kMost;
     static_assert(kTimes % kBatch == 0, "");
-    const int64_t end = a.out_type == kOutMx ? mx_padded(a.N) : a.N;
+    typedef typename std::conditional<MX, double, float>::type value;
+    const int64_t end = MX ? mx_padded(a.N) : a.N;
     const int q = lane % kPer;
     const int64_t n = (GLU ? c0 / 2 : c0) + q * 8;
     if (n >= end) return;
     const float *bias = a.bias[d] + (int64_t)j * a.NW;
-    const auto take = [&](int r, int at, float(&y)[8]) {
-        const f32x4 lo = sums[chunk<COLS>(r, at)], hi = sums[chunk<COLS>(r, at + 1)];
+    const auto take = [&](int r, int at, value(&y)[8]) {
+        const f32x4 v[2] = {sums[chunk<COLS>(r, at)], sums[chunk<COLS>(r, at + 1)]};
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            y[i] = lo[i];
-            y[i + 4] = hi[i];
+        for (int i = 0; i < 8; i++) y[i] = v[i / 4][i % 4];
+        if constexpr (TWO) {
+            const f32x4 l[2] = {low[chunk<COLS>(r, at)], low[chunk<COLS>(r, at + 1)]};
+#pragma unroll
+            for (int i = 0; i < 8; i++) y[i] += l[i / 4][i % 4];
         }
     };
     // gated: blocks of 16 gate and 16 up columns alternate
     const int at = GLU ? (q >> 1) * 8 + (q & 1) * 2 : q * 2;
-#pragma unroll
+#pragma unroll(MX ? 1 : kTimes)
     for (int r0 = 0; r0 < kTimes * kStep; r0 += kBatch * kStep) {
-        float y[kBatch][8], up[GLU ? kBatch : 1][8];
+        value y[kBatch][8], up[GLU ? kBatch : 1][8];
 #pragma unroll
         for (int b = 0; b < kBatch; b++) {
             take(r0 + b * kStep + lane / kPer, at, y[b]);
@@ -154,23 +217,33 @@ __device__ __forceinline__ void emit_rows(const MxExpertArgs &a, const f32x4 *su
             if constexpr (GLU) {
                 if (a.has_bias) add_bias(a, bias + a.N, n, up[b]);
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[b][i] = y[b][i] * sigmoid(y[b][i]) * up[b][i];
+                for (int i = 0; i < 8; i++)
+                    if constexpr (MX) y[b][i] = silu_wide(y[b][i]) * up[b][i];
+                    else y[b][i] = y[b][i] * sigmoid(y[b][i]) * up[b][i];
             } else if (a.act != A2AV_ACT_NONE) {
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[b][i] = act_of(a.act, y[b][i]);
+                for (int i = 0; i < 8; i++)
+                    if constexpr (MX) y[b][i] = act_wide(a.act, y[b][i]);
+                    else y[b][i] = act_of(a.act, y[b][i]);
             }
-            put_out(a, d, row0 + m, n, y[b]);
+            if constexpr (MX) put_mx(a, d, row0 + m, n, y[b]);
+            else put_out(a, d, row0 + m, n, y[b]);
         }
     }
 }
-template <int ROWS, int COLS, typename RowOf>
-__device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, int d, int j, int64_t row0, int64_t M,
-                                     int64_t c0, int lane, RowOf row_of) {
-    if (a.act == A2AV_ACT_SWIGLU) emit_rows<ROWS, COLS, true>(a, sums, d, j, row0, M, c0, lane, row_of);
-    else emit_rows<ROWS, COLS, false>(a, sums, d, j, row0, M, c0, lane, row_of);
+template <int ROWS, int COLS, bool MX, bool TWO, typename RowOf>
+__device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, const f32x4 *low, int d, int j, int64_t row0,
+                                     int64_t M, int64_t c0, int lane, RowOf row_of) {
+    if (a.act == A2AV_ACT_SWIGLU) emit_rows<ROWS, COLS, true, MX, TWO>(a, sums, low, d, j, row0, M, c0, lane, row_of);
+    else emit_rows<ROWS, COLS, false, MX, TWO>(a, sums, low, d, j, row0, M, c0, lane, row_of);
 }
 
 // ------------------------------------------------------------------ the tiles
+// Bound by the matrix cores, their operands' LDS reads and the clock under their power:
+// 32 experts of 512 rows, K 7168, 4096 columns: 4-bit rows 271 us (3.5 PFLOP/s), 8-bit
+// ones 380 (2.5), with 8-bit outputs, two products an element, 769; K 2048, 7168
+// columns 187 and 243. Without the loads the first would take 180, with all of them
+// in the L2 240; spreading them over a step, or two steps further ahead, changes nothing.
 // Tiles of BM rows and BC columns. LDS rows are 128 bytes of an operand's row: 256
 // elements of e2m1 or 128 of e4m3, so that a step is 256 elements of 4-bit rows or
 // 128 of 8-bit ones, and every second step of those takes new weights. Buffer
@@ -287,7 +360,7 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
                                             typename MxShape<FORMAT, BM, BC, WM, WC>::B &ob,
                                             MxScales<BM, BC> &os, unsigned char *const (&sa)[2],
                                             unsigned char *const (&sb)[2], u32x4 *ss, int macros,
-                                            f32x16 (&acc)[MxShape<FORMAT, BM, BC, WM, WC>::kBlocksM][2]) {
+                                            f32x16 (&acc)[1 + SPLIT][MxShape<FORMAT, BM, BC, WM, WC>::kBlocksM][2]) {
     typedef MxShape<FORMAT, BM, BC, WM, WC> S;
     typedef typename MxFrag<FORMAT>::type frag;
     constexpr bool k8 = FORMAT == A2AV_MX_FP8;
@@ -408,17 +481,17 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
                 const Split &x = parts[p & 1];
 #pragma unroll
                 for (int c = 0; c < 2; c++)
-                    acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], x.hi, acc[m][c], wb[kSet][c][kWord],
-                                                       wa[kSet][m][kWord]);
+                    acc[0][m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], x.hi, acc[0][m][c], wb[kSet][c][kWord],
+                                                          wa[kSet][m][kWord]);
 #pragma unroll
                 for (int c = 0; c < 2; c++)
-                    acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], x.lo, acc[m][c], wb[kSet][c][kWord],
-                                                       wa[kSet][m][kWord]);
+                    acc[1][m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], x.lo, acc[1][m][c], wb[kSet][c][kWord],
+                                                          wa[kSet][m][kWord]);
             } else {
 #pragma unroll
                 for (int c = 0; c < 2; c++)
-                    acc[m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], fa[p % kRing], acc[m][c], wb[kSet][c][kWord],
-                                                       wa[kSet][m][kWord]);
+                    acc[0][m][c] = mfma_at<FORMAT, kByte>(fb[q & 1][c], fa[p % kRing], acc[0][m][c], wb[kSet][c][kWord],
+                                                          wa[kSet][m][kWord]);
             }
             if constexpr (kPipe) {
                 parts[(p + 1) & 1] = split(fa[(p + 1) % kRing]);
@@ -454,9 +527,10 @@ __device__ __forceinline__ void mx_contract(typename MxShape<FORMAT, BM, BC, WM,
     wait_for<0, true>();
 }
 
-template <int FORMAT, bool SPLIT, int BM, int BC, int WM, int WC>
+template <int FORMAT, bool MX, int BM, int BC, int WM, int WC>
 __global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs a) {
     typedef MxShape<FORMAT, BM, BC, WM, WC> S;
+    constexpr bool SPLIT = MX && FORMAT == A2AV_MX_FP8;
     __shared__ __align__(16) unsigned char a0[BM * 128], a1[BM * 128], b0[BC * 128], b1[BC * 128];
     __shared__ u32x4 ss[4 * S::kScaleRows];
     unsigned char *const sa[2] = {a0, a1}, *const sb[2] = {b0, b1};
@@ -497,7 +571,7 @@ __global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs
         os.last_x = (int)(a.x_stride - x_bytes) - 16;
         os.last_w = (int)(a.w_stride - padded / 2) - 16;
     }
-    f32x16 acc[S::kBlocksM][2] = {};
+    f32x16 acc[1 + SPLIT][S::kBlocksM][2] = {};
     const int macros = (int)(padded / kMxPad);
     if (S::kBlocksM >= 4 && left <= WM * 32)
         mx_contract<FORMAT, SPLIT, BM, BC, WM, WC, 1>(oa, ob, os, sa, sb, ss, macros, acc);
@@ -507,22 +581,36 @@ __global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs
         mx_contract<FORMAT, SPLIT, BM, BC, WM, WC, S::kBlocksM>(oa, ob, os, sa, sb, ss, macros, acc);
     __syncthreads();
     // in passes of kPass row blocks, each wave in its own part of the stages
-    constexpr int kPass = S::kBlocksM < 2 ? 1 : 2, kPart = kPass * 32 * 64 * 16 / 4, kParts = S::kWaves / 4;
-    static_assert(kParts * kPart <= BM * 128 && kParts * kPart <= BC * 128, "");
+    constexpr int kPass = SPLIT || S::kBlocksM < 2 ? 1 : 2, kPlane = kPass * 32 * 64 * 4, kParts = S::kWaves / 4;
+    constexpr bool kSpare = SPLIT && kPlane == BM * 128;  // the second sums of the last wave have no room in them
+    static_assert(kParts * kPlane <= BM * 128 && (SPLIT ? 2 : 1) * kParts * kPlane <= BC * 128, "");
+    static_assert(!SPLIT || (kParts == 1 && (kSpare || 2 * kPlane <= BM * 128)), "");
+    __shared__ __align__(16) unsigned char spare[kSpare ? 2 * kPlane : 16];
     const int in = wave / kParts;
-    f32x4 *sums = (f32x4 *)((in == 0 ? a0 : in == 1 ? a1 : in == 2 ? b0 : b1) + wave % kParts * kPart);
-#pragma unroll
-    for (int p = 0; p < S::kBlocksM / kPass; p++) {
-        if (p * kPass * WM * 32 >= left) break;
+    f32x4 *sums, *low;
+    if constexpr (kSpare) {
+        sums = (f32x4 *)(in == 0 ? a0 : in == 1 ? b0 : in == 2 ? b1 : spare);
+        low = (f32x4 *)(in == 0 ? a1 : (in == 1 ? b0 : in == 2 ? b1 : spare) + kPlane);
+    } else {
+        sums = (f32x4 *)((in == 0 ? a0 : in == 1 ? a1 : in == 2 ? b0 : b1) + wave % kParts * kPlane);
+        low = sums + kPlane / 16;
+    }
+    const auto pass = [&](auto number) __attribute__((always_inline)) {
+        constexpr int p = decltype(number)::value;
+        if (p * kPass * WM * 32 >= left) return;
 #pragma unroll
         for (int u = 0; u < kPass; u++)
 #pragma unroll
-            for (int v = 0; v < 2; v++) put_sums<64>(sums, u, v, acc[p * kPass + u][v], lane);
+            for (int v = 0; v < 2; v++) {
+                put_sums<64>(sums, u, v, acc[0][p * kPass + u][v], lane);
+                if constexpr (SPLIT) put_sums<64>(low, u, v, acc[1][p * kPass + u][v], lane);
+            }
         asm volatile("" ::: "memory");
-        emit<kPass * 32, 64>(a, sums, d, j, row0, M, c0 + wc * 64, lane,
-                             [&](int r) { return m0 + ((p * kPass + (r >> 5)) * WM + wm) * 32 + (r & 31); });
+        emit<kPass * 32, 64, MX, SPLIT>(a, sums, low, d, j, row0, M, c0 + wc * 64, lane,
+                                        [&](int r) { return m0 + ((p * kPass + (r >> 5)) * WM + wm) * 32 + (r & 31); });
         asm volatile("" ::: "memory");
-    }
+    };
+    each(pass, std::make_integer_sequence<int, S::kBlocksM / kPass>{});
 }
 
 // ------------------------------------------------------------------ few rows
@@ -600,14 +688,17 @@ __device__ __forceinline__ bool find_tile(const MxExpertArgs &a, uint32_t t, Few
     return f.expert >= 0;
 }
 
-template <int FORMAT, bool GLU>
+template <int FORMAT, bool GLU, bool MX>
 __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertArgs a) {
     constexpr int kFrags = GLU ? 4 : 2, kCols = kFrags * 16, kChunks = kFewRows * kCols / 4;
     constexpr bool k8 = FORMAT == A2AV_MX_FP8;
     constexpr int kThreads = kFewWaves * kWave, kScaleRows = kCols + kFewRows;
     constexpr int kScaleLoads = (kScaleRows * kFewMacros / 2 + kThreads - 1) / kThreads;  // of 16 bytes a thread
-    __shared__ f32x4 sums[kFewWaves][kChunks];
-    __shared__ __align__(16) unsigned char scales[kScaleRows * kFewScaleRow];
+    constexpr bool kTwo = MX && k8;
+    // the scales, and then the waves' sums
+    constexpr int kSums = (1 + kTwo) * kFewWaves * kChunks * 16, kScales = kScaleRows * kFewScaleRow;
+    __shared__ __align__(16) unsigned char scales[kSums > kScales ? kSums : kScales];
+    f32x4 *const sums = (f32x4 *)scales;  // [waves][1 or 2][kChunks]
     if (status_at_entry(a.status)) return;
     const uint32_t t = blockIdx.x / (uint32_t)a.cols, ct = blockIdx.x - t * a.cols;
     FewTile tile;
@@ -624,7 +715,7 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
     const rsrc_t bw[2] = {buffer(w, (uint32_t)cols * ws), buffer(w + (GLU ? a.N * a.w_stride : 0), (uint32_t)cols * ws)};
     const uint32_t padded = (uint32_t)mx_padded(a.K), w_scales = padded / 2, x_scales = k8 ? padded : padded / 2;
     const int macros = (int)(padded / kMxPad);
-    f32x4 acc[kFrags] = {};
+    f32x4 acc[1 + kTwo][kFrags] = {};
     for (int from = 0; from < macros; from += kFewMacros) {
         const int to = min(from + kFewMacros, macros);
         // the scales of all rows for these steps, sixteen bytes a load, rows along the threads
@@ -692,29 +783,49 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
                     const Split x = split(x8);
 #pragma unroll
                     for (int f = 0; f < kFrags; f++) {
-                        acc[f] = mfma_few<FORMAT>(fw[f][s], x.hi, acc[f], sw[f].x >> (s * 8), sx.x >> (s * 8));
-                        acc[f] = mfma_few<FORMAT>(fw[f][s], x.lo, acc[f], sw[f].x >> (s * 8), sx.x >> (s * 8));
+                        acc[0][f] = mfma_few<FORMAT>(fw[f][s], x.hi, acc[0][f], sw[f].x >> (s * 8), sx.x >> (s * 8));
+                        acc[kTwo][f] = mfma_few<FORMAT>(fw[f][s], x.lo, acc[kTwo][f], sw[f].x >> (s * 8), sx.x >> (s * 8));
                     }
                 } else {
 #pragma unroll
                     for (int f = 0; f < kFrags; f++)
-                        acc[f] = mfma_few<FORMAT>(fw[f][s], x8, acc[f], sw[f].x >> (s * 8), sx.x >> (s * 8));
+                        acc[0][f] = mfma_few<FORMAT>(fw[f][s], x8, acc[0][f], sw[f].x >> (s * 8), sx.x >> (s * 8));
                 }
             }
         }
     }
-#pragma unroll
-    for (int f = 0; f < kFrags; f++) sums[wave][chunk<kCols>(lane & 15, f * 4 + quarter)] = acc[f];
     __syncthreads();
-    for (int k = threadIdx.x; k < kChunks; k += kThreads) {
-        f32x4 y = sums[0][k];
 #pragma unroll
-        for (int i = 1; i < kFewWaves; i++) y += sums[i][k];
-        sums[0][k] = y;
+    for (int p = 0; p <= kTwo; p++)
+#pragma unroll
+        for (int f = 0; f < kFrags; f++)
+            sums[(wave * (1 + kTwo) + p) * kChunks + chunk<kCols>(lane & 15, f * 4 + quarter)] = acc[p][f];
+    __syncthreads();
+    // with two sums in double, which leave as two numbers again
+    for (int k = threadIdx.x; k < kChunks; k += kThreads) {
+        if constexpr (kTwo) {
+            f32x4 y, rest;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                double t = 0.0;
+#pragma unroll
+                for (int i = 0; i < 2 * kFewWaves; i++) t += (double)sums[i * kChunks + k][c];
+                y[c] = (float)t;
+                rest[c] = (float)(t - y[c]);  // (of an infinity NaN, as the block becomes)
+            }
+            sums[k] = y;
+            sums[kChunks + k] = rest;
+        } else {
+            f32x4 y = sums[k];
+#pragma unroll
+            for (int i = 1; i < kFewWaves; i++) y += sums[i * kChunks + k];
+            sums[k] = y;
+        }
     }
     __syncthreads();
     if (wave != 0) return;
-    emit_rows<kFewRows, kCols, GLU>(a, sums[0], d, j, row0, rows, (int64_t)ct * kCols, lane, [](int r) { return (int64_t)r; });
+    emit_rows<kFewRows, kCols, GLU, MX, kTwo>(a, sums, sums + kChunks, d, j, row0, rows, (int64_t)ct * kCols, lane,
+                                              [](int r) { return (int64_t)r; });
 }
 
 // ------------------------------------------------------------------ host
@@ -728,13 +839,16 @@ static int64_t product_columns(const MxExpertArgs &a) {
 enum { kBig, kMid, kSmall, kFew };
 constexpr int kRows[] = {256, 128, 64, kFewRows}, kCols[] = {256, 128, 128};
 
+// Of 8-bit rows with outputs of 8 bits there are no tiles of 256: their two sums would
+// take all registers (16384 ragged rows on 32 experts, K 7168, 4096 columns: 757 us in
+// tiles of 128; with one sum in tiles of 256 745; equal experts 769 and 705).
 // The largest tile of which the product has enough to fill the compute units, R
 // rows over n experts, C product columns, and which the mean expert more than half
 // fills (32 experts of 64, 128 and 192 rows, 4-bit rows, K 7168, 4096 columns: 106,
 // 164 and 210 us in tiles of 64, 107, 125 and 175 of 128, 114, 127 and 146 of 256; of
 // 8-bit rows with K 2048 and 7168 columns 69, 103, 141; 69, 87, 124; 78, 93, 132).
-static int shape_of(int64_t R, int64_t n, int64_t C) {
-    for (int s = R <= 64 * n ? kSmall : R <= 128 * n ? kMid : kBig; s < kSmall; s++) {
+static int shape_of(int64_t R, int64_t n, int64_t C, bool two) {
+    for (int s = R <= 64 * n ? kSmall : R <= 128 * n || two ? kMid : kBig; s < kSmall; s++) {
         const int64_t t = kRows[s], cols = (C + kCols[s] - 1) / kCols[s];
         const int64_t tiles = R / t + (R % (n * t) ? n / 2 : 0);
         if (tiles * cols >= 200) return s;
@@ -742,19 +856,29 @@ static int shape_of(int64_t R, int64_t n, int64_t C) {
     return kSmall;
 }
 
-template <int FORMAT>
+template <int FORMAT, bool MX>
 static void launch_few(const MxExpertArgs &a, int64_t tiles, hipStream_t stream) {
-    const dim3 g((unsigned)(tiles ? tiles * a.cols : 1));  // without rows the offsets are still checked
-    if (a.act == A2AV_ACT_SWIGLU) hipLaunchKernelGGL((k_mx_few<FORMAT, true>), g, dim3(kFewWaves * kWave), 0, stream, a);
-    else hipLaunchKernelGGL((k_mx_few<FORMAT, false>), g, dim3(kFewWaves * kWave), 0, stream, a);
+    const dim3 g((unsigned)(tiles ? tiles * a.cols : 1)), b(kFewWaves * kWave);  // without rows the offsets are still checked
+    if (a.act == A2AV_ACT_SWIGLU) hipLaunchKernelGGL((k_mx_few<FORMAT, true, MX>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_mx_few<FORMAT, false, MX>), g, b, 0, stream, a);
 }
 
-template <int FORMAT, bool SPLIT>
+template <int FORMAT, bool MX>
 static void launch_tile(const MxExpertArgs &a, int shape, int64_t tiles, hipStream_t stream) {
     const dim3 g((unsigned)((tiles * a.cols + 7) / 8 * 8));
-    if (shape == kBig) hipLaunchKernelGGL((k_mx_tile<FORMAT, SPLIT, 256, 256, 2, 4>), g, dim3(512), 0, stream, a);
-    else if (shape == kMid) hipLaunchKernelGGL((k_mx_tile<FORMAT, SPLIT, 128, 128, 2, 2>), g, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((k_mx_tile<FORMAT, SPLIT, 64, 128, 2, 2>), g, dim3(256), 0, stream, a);
+    if constexpr (FORMAT == A2AV_MX_FP4 || !MX)
+        if (shape == kBig) {
+            hipLaunchKernelGGL((k_mx_tile<FORMAT, MX, 256, 256, 2, 4>), g, dim3(512), 0, stream, a);
+            return;
+        }
+    if (shape == kMid) hipLaunchKernelGGL((k_mx_tile<FORMAT, MX, 128, 128, 2, 2>), g, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_mx_tile<FORMAT, MX, 64, 128, 2, 2>), g, dim3(256), 0, stream, a);
+}
+
+template <int FORMAT, bool MX>
+static void launch(const MxExpertArgs &a, int shape, int64_t tiles, hipStream_t stream) {
+    if (shape == kFew) launch_few<FORMAT, MX>(a, tiles, stream);
+    else launch_tile<FORMAT, MX>(a, shape, tiles, stream);
 }
 
 }  // namespace a2av
@@ -810,7 +934,8 @@ A2AV_API int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_form
     a.P = P;
     int64_t R = 0;
     for (int d = 0; d < W; d++) R += a.x_rows[d] = x_rows[d];
-    int shape = R <= 12 * (int64_t)W * P ? kFew : shape_of(R, (int64_t)W * P, product_columns(a));
+    const bool mx = a.out_type == kOutMx, two = mx && x_format == A2AV_MX_FP8;
+    int shape = R <= 12 * (int64_t)W * P ? kFew : shape_of(R, (int64_t)W * P, product_columns(a), two);
     const auto tiles_of = [&](int s) {
         const int64_t t = most_tiles(x_rows, W, P, kRows[s]);
         return R < t ? R : t;
@@ -819,18 +944,15 @@ A2AV_API int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_form
         const int64_t n = a.out_type == kOutMx ? mx_padded(N) : N;
         return s == kFew ? (n + kFewCols - 1) / kFewCols : (product_columns(a) + kCols[s] - 1) / kCols[s];
     };
-    while (shape > kBig && tiles_of(shape) * cols_of(shape) > kMostGroups) shape--;
+    while (shape > (two ? kMid : kBig) && tiles_of(shape) * cols_of(shape) > kMostGroups) shape--;
     const int64_t tiles = tiles_of(shape);
     a.cols = (int)cols_of(shape);
     if (tiles * a.cols > kMostGroups) return A2AV_EARG;
-    if (shape == kFew) {
-        if (x_format == A2AV_MX_FP8) launch_few<A2AV_MX_FP8>(a, tiles, stream);
-        else launch_few<A2AV_MX_FP4>(a, tiles, stream);
-    } else {
+    if (shape != kFew)
         launch_plan(W, P, x_rows, expert_offsets, kRows[shape], (unsigned char *)workspace, l, status, stream);
-        if (x_format == A2AV_MX_FP4) launch_tile<A2AV_MX_FP4, false>(a, shape, tiles, stream);
-        else if (a.out_type == kOutMx) launch_tile<A2AV_MX_FP8, true>(a, shape, tiles, stream);
-        else launch_tile<A2AV_MX_FP8, false>(a, shape, tiles, stream);
-    }
+    if (x_format == A2AV_MX_FP4 && mx) launch<A2AV_MX_FP4, true>(a, shape, tiles, stream);
+    else if (x_format == A2AV_MX_FP4) launch<A2AV_MX_FP4, false>(a, shape, tiles, stream);
+    else if (mx) launch<A2AV_MX_FP8, true>(a, shape, tiles, stream);
+    else launch<A2AV_MX_FP8, false>(a, shape, tiles, stream);
     return hipGetLastError() == hipSuccess ? A2AV_OK : A2AV_EHIP;
 }

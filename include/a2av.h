@@ -846,7 +846,9 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  * with A2AV_ACT_SWIGLU as moe_expert_linear has it (2N weight rows, N outputs).
  * Eight neighbouring products are summed exactly; but of A2AV_MX_FP8 rows with
  * an out of 16 bits a sum of eight may drop what lies more than 2^14 below its
- * largest product (5e-6 of random sums, a thousandth of out's rounding).
+ * largest product (5e-6 of random sums, a thousandth of out's rounding). For an
+ * out of 8 bits the products of A2AV_MX_FP8 elements of 2 and above and those of
+ * smaller ones have an fp32 sum each, added in double, and act is in double.
  * The products read the elements as they lie: a block that stands for NaN gives
  * NaN where its row or column goes.
  *   K, N            1 .. A2AV_MAX_WIDTH

@@ -42,7 +42,7 @@ struct MxExpertArgs {
     int64_t x_stride, w_stride, out_stride;  // bytes of a row; of out if microscaled
     int W, P;
     int act, out_type, has_bias;
-    int wide;  // out and bias by 16-byte vectors
+    int wide;  // out by 16-byte vectors
     int cols;  // column tiles
 };
 
@@ -167,11 +167,13 @@ __device__ __forceinline__ void put_out(const MxExpertArgs &a, int d, int64_t ro
         if (n + i < a.N) out[i] = a.out_type == kOutBf16 ? Bf16::from_float(y[i]) : Fp16::from_float(y[i]);
 }
 
+// (the columns of a row's padding have no bias)
 template <typename T>
 __device__ __forceinline__ void add_bias(const MxExpertArgs &a, const float *bias, int64_t n, T (&y)[8]) {
+    const bool whole = n + 8 <= a.N;
 #pragma unroll
     for (int i = 0; i < 8; i++)
-        if (a.wide || n + i < a.N) y[i] += bias[n + i];
+        if (whole || n + i < a.N) y[i] += bias[n + i];
 }
 
 // The rows of a pass; `row_of(r)` is the expert's row behind LDS row r, c0 the
@@ -924,7 +926,7 @@ A2AV_API int moe_expert_linear_mx(int W, int P, int64_t K, int64_t N, int x_form
         a.weight[d] = (const unsigned char *)weight[d];
         a.bias[d] = bias ? bias[d] : nullptr;
         a.out[d] = out[d];
-        a.wide = a.wide && aligned16(a.bias[d]) && aligned16(out[d]);
+        a.wide = a.wide && aligned16(out[d]);
     }
     a.offsets = expert_offsets;
     a.tiles = (const int32_t *)workspace;

@@ -872,7 +872,8 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  * Arrays that are written overlap no others (out at the base of x: A2AV_EARG).
  * Two kernels: the plan of moe_expert_linear, and the products on matrix cores;
  * their tiles are chosen for as many rows as x_rows allows (more than 2^22 of
- * 256 x 256 that x_rows and the experts could need: A2AV_EARG). Where x_rows
+ * 256 x 256, or of 128 x 128 from A2AV_MX_FP8 to it, that x_rows and the experts
+ * could need: A2AV_EARG). Where x_rows
  * allows at most 12 rows an expert it is one kernel, which reads the offsets
  * itself.
  */

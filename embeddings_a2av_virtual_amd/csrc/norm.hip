@@ -237,7 +237,7 @@ __global__ __launch_bounds__(1024) void k_norm_any(const NormArgs a) {
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const scalar *x = (const scalar *)a.x[rank] + t * a.H;
         const scalar *residual = (const scalar *)a.residual[rank] + t * a.H;
-        scalar *sum = (scalar *)a.sum[rank] + t * a.H, *out = (scalar *)a.out[rank] + t * a.H;
+        scalar *sum = (scalar *)a.sum[rank] + t * a.H;
         const auto added = [&](int64_t c) {
             vec h = load_row<E>(x, c, a.H);
             if (a.has_residual) {

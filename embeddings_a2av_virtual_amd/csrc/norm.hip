@@ -140,7 +140,7 @@ __device__ __forceinline__ void put_norm(const NormArgs &a, int rank, int64_t t,
 // Bound by the bytes: 8 x 2048 rows of 7168 in bf16 with a residual, the sum and 8-bit
 // rows 142 us, 5.8 TB/s (a copy reaches 6.5; 150 with stores of the rows that stay in
 // the caches, 162 with a workgroup for every row and no load ahead); 8 x 8192 of 2048
-// 158, 6.0; odd ones 8 x 2048 x 1003 in fp16 28 (39 read twice). One row of 7168 takes
+// 157, 6.0; odd ones 8 x 2048 x 1003 in fp16 25 (39 read twice). One row of 7168 takes
 // 4 us. Without a residual the arithmetic shows: 93 us, 3.8 TB/s.
 template <typename E, int FORMAT, int VPT, int MOST, bool WHOLE>
 __global__ __launch_bounds__(MOST == kWave ? 256 : MOST) void k_norm_row(const NormArgs a) {
@@ -163,7 +163,10 @@ __global__ __launch_bounds__(MOST == kWave ? 256 : MOST) void k_norm_row(const N
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
             const int c = min(i * lanes + lane, own - 1) * 8;
-            if constexpr (WHOLE) to[i] = E::load(p + c);
+            // (8 x 1024 rows of 7168 in fp32: 141 us, 159 with loads past the caches; in 16 bits
+            // those are the better ones, 142 and 146)
+            if constexpr (WHOLE && E::kExact) to[i] = E::load(p + c);
+            else if constexpr (WHOLE) to[i] = E::cached(p + c);
             else to[i] = load_row<E>(p, c, a.H);
         }
     };
@@ -529,9 +532,10 @@ static void launch_norm(const NormArgs &a, int W, int format, hipStream_t stream
     else launch_norm<E, 0>(a, W, stream);
 }
 
-// The gradient's: a wave each up to 2048 elements, else a workgroup with two vectors a
-// thread, which leaves registers for the next row, and one where there are few rows
-// of whole vectors.
+// The gradient's: a wave each up to 2048 elements (fewer workgroups, whose weight sums
+// have to be read again: 1021 rows of 1111 in fp32 13.1 us, 18.8 with a workgroup for
+// each), else a workgroup with two vectors a thread, which leaves registers for the
+// next row, and one where there are few rows of whole vectors.
 struct GradShape {
     bool wave;
     int per, threads;
@@ -541,8 +545,8 @@ static GradShape grad_shape(int W, int64_t T, int64_t H) {
     const int64_t vecs = (H + 7) / 8, rows = (int64_t)W * T;
     const bool whole = H % 8 == 0;
     GradShape s = {};
-    s.wave = vecs <= 128 || (whole && vecs <= 256 && rows >= 2048);
-    s.per = !whole ? 2 : s.wave ? (int)((vecs + kWave - 1) / kWave) : vecs <= 1024 && rows < 2048 ? 1 : 2;
+    s.wave = vecs <= 256 && in_registers(H);
+    s.per = !whole ? (s.wave && vecs > 128 ? 4 : 2) : s.wave ? (int)((vecs + kWave - 1) / kWave) : vecs <= 1024 && rows < 2048 ? 1 : 2;
     if (!in_registers(H)) s.threads = 1024;
     else s.threads = s.wave ? 256 : (int)((vecs + s.per * kWave - 1) / (s.per * kWave) * kWave);
     s.most = up_to(rows, kGradWaves / (s.threads / kWave) / 256 * 256);
@@ -555,7 +559,9 @@ static void launch_grad(const NormGradArgs &a, int W, hipStream_t stream) {
     const GradShape s = grad_shape(W, a.T, a.H);
     const dim3 g((unsigned)a.groups), b((unsigned)s.threads);
     if (!in_registers(a.H)) hipLaunchKernelGGL(k_norm_grad_any<E>, g, b, 0, stream, a);
-    else if (a.H % 8 != 0 && s.wave) hipLaunchKernelGGL((k_norm_grad_row<E, 2, kWave, false>), g, b, 0, stream, a);
+    else if (a.H % 8 != 0 && s.wave && s.per == 2)
+        hipLaunchKernelGGL((k_norm_grad_row<E, 2, kWave, false>), g, b, 0, stream, a);
+    else if (a.H % 8 != 0 && s.wave) hipLaunchKernelGGL((k_norm_grad_row<E, 4, kWave, false>), g, b, 0, stream, a);
     else if (a.H % 8 != 0 && b.x <= 512) hipLaunchKernelGGL((k_norm_grad_row<E, 2, 512, false>), g, b, 0, stream, a);
     else if (a.H % 8 != 0) hipLaunchKernelGGL((k_norm_grad_row<E, 2, 1024, false>), g, b, 0, stream, a);
     else if (s.wave && s.per == 1) hipLaunchKernelGGL((k_norm_grad_row<E, 1, kWave, true>), g, b, 0, stream, a);

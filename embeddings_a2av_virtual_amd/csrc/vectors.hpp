@@ -15,7 +15,8 @@ typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // An element type: `vec` holds eight of them as they lie in memory. What is loaded
-// and stored is not used again soon.
+// and stored is not used again soon, but for the lines of `cached` loads, which come in
+// two halves or are shared with a neighbour.
 struct ElemF32 {
     static constexpr bool kExact = false;  // the product of two is exact in fp32
     typedef float scalar;
@@ -24,6 +25,9 @@ struct ElemF32 {
     };
     static __device__ __forceinline__ vec load(const scalar *p) {
         return {__builtin_nontemporal_load((const f32x4_any *)p), __builtin_nontemporal_load((const f32x4_any *)p + 1)};
+    }
+    static __device__ __forceinline__ vec cached(const scalar *p) {
+        return {*(const f32x4_any *)p, *((const f32x4_any *)p + 1)};
     }
     static __device__ __forceinline__ void store(scalar *p, vec v) {
         __builtin_nontemporal_store(v.lo, (f32x4_any *)p);
@@ -43,6 +47,7 @@ struct Elem16 {
     typedef uint16_t scalar;
     typedef u16x8 vec;
     static __device__ __forceinline__ vec load(const scalar *p) { return __builtin_nontemporal_load((const u16x8_any *)p); }
+    static __device__ __forceinline__ vec cached(const scalar *p) { return *(const u16x8_any *)p; }
     static __device__ __forceinline__ void store(scalar *p, vec v) { __builtin_nontemporal_store(v, (u16x8_any *)p); }
     static __device__ __forceinline__ void put(vec &v, int i, scalar x) { v[i] = x; }
     static __device__ __forceinline__ scalar raw(const vec &v, int i) { return v[i]; }
@@ -65,7 +70,7 @@ struct ElemF16 : Elem16 {
 // not stored.
 template <typename E>
 __device__ __forceinline__ typename E::vec load_row(const typename E::scalar *p, int64_t c, int64_t H) {
-    if (c + 8 <= H) return E::load(p + c);
+    if (c + 8 <= H) return E::cached(p + c);
     typename E::vec v = {};
 #pragma unroll
     for (int i = 0; i < 8; i++)

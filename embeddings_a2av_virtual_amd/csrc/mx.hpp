@@ -98,13 +98,13 @@ __device__ __forceinline__ uint32_t quad_top(const float (&v)[8]) {
     return quad_max(m);
 }
 
-// The same where no value is NaN.
+// The same by the maximum that gives NaN if an operand is: half the instructions.
 __device__ __forceinline__ uint32_t quad_largest(const float (&v)[8]) {
     float m;
-    asm("v_max3_f32 %0, |%1|, |%2|, 0" : "=v"(m) : "v"(v[0]), "v"(v[1]));
+    asm("v_maximum3_f32 %0, |%1|, |%2|, 0" : "=v"(m) : "v"(v[0]), "v"(v[1]));
 #pragma unroll
-    for (int i = 2; i < 8; i += 2) asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(v[i]), "v"(v[i + 1]));
-    return quad_max(__float_as_uint(m));
+    for (int i = 2; i < 8; i += 2) asm("v_maximum3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(v[i]), "v"(v[i + 1]));
+    return quad_max(__float_as_uint(m) & 0x7FFFFFFFu);
 }
 
 // The scale byte of a block whose largest magnitude has these bits, and the

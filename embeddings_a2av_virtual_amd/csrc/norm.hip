@@ -61,18 +61,13 @@ struct RowScale {
     }
 };
 
-// A lane's eight weights, and whether one of them is NaN.
+// A lane's eight weights.
 struct Weights {
     float v[8];
-    bool nan;
     template <typename E>
     __device__ __forceinline__ void set(const typename E::vec &w) {
-        nan = false;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[i] = E::get(w, i);
-            nan = nan || v[i] != v[i];
-        }
+        for (int i = 0; i < 8; i++) v[i] = E::get(w, i);
     }
 };
 
@@ -99,10 +94,8 @@ __device__ __forceinline__ void put_norm(const NormArgs &a, int rank, int64_t t,
         }
         if constexpr (FORMAT != 0) {
             int scale;
-            // Of elements one that is NaN makes the row's factor NaN; of weights it is told.
-            // A block behind the row is 0, also where the row has no finite factor.
-            const uint32_t top = quad_largest(y), nan = quad_max(w.nan ? 0x7FC00000u : 0u);
-            const auto p = mx_block<FORMAT>(y, nan > top ? nan : top, (c & ~(int64_t)31) < a.H ? s.rest : 0.0, scale);
+            // a block behind the row is 0, also where the row has no finite factor
+            const auto p = mx_block<FORMAT>(y, quad_largest(y), (c & ~(int64_t)31) < a.H ? s.rest : 0.0, scale);
             unsigned char *row = a.rows[rank] + t * mx_stride(FORMAT, a.H);
             __builtin_nontemporal_store(p, (typename Mx<FORMAT>::packed *)(row + c / 8 * (int64_t)sizeof(p)));
             if (threadIdx.x % 4 == 0) row[mx_element_bytes(FORMAT, a.H) + c / kMxBlock] = (unsigned char)scale;

@@ -45,17 +45,18 @@ __device__ __forceinline__ double inverse_root(double m) {
 }
 
 // What a row is multiplied by, r = 1 / sqrt(mean(h^2) + eps), in two steps: a power
-// of two and the rest in double. In types of 16 bits h * power * w is then exact in
-// fp32 and inside its range (down to 2^-133, where y is below 2^-100), so that an
-// element of a block takes one product in double. The power is 1 unless the row's
-// magnitude is out of the ordinary.
+// of two and the rest in double, from 1 to 2 (1/4 to 64 at the ends of bf16's range). In
+// types of 16 bits h * power * w is then exact in fp32 and not past its range where y is
+// not, so that an element of a block takes one product in double; but for a y below
+// 2^-132 and elements 2^-140 below their row's magnitude. (A branch for the power 1 cost
+// what it saved: 91.3 us without a residual with it, 90.4 without.)
 struct RowScale {
     double r, rest;
     float power;
-    __device__ __forceinline__ RowScale(double mean) {  // of h^2, and eps
+    __device__ __forceinline__ explicit RowScale(double mean) {  // of h^2, and eps
         r = inverse_root(mean);
         int k = (int)(upper_word(r) >> 20) - 1023;  // NaN, infinity and 0 at the ends
-        k = k < -32 ? (k < -112 ? -112 : k - 12) : k > 32 ? (k > 88 ? 88 : k - 12) : 0;
+        k = min(max(k, -126), 127);
         power = __uint_as_float((uint32_t)(127 + k) << 23);
         rest = r * __longlong_as_double((int64_t)(1023 - k) << 52);
     }
@@ -78,13 +79,8 @@ __device__ __forceinline__ void put_norm(const NormArgs &a, int rank, int64_t t,
                                          const Weights &w, const RowScale &s) {
     if constexpr (E::kExact) {
         float y[8];
-        if (s.power == 1.0f) {  // of the whole row
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = E::get(h, i) * w.v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = E::get(h, i) * s.power * w.v[i];
-        }
+        for (int i = 0; i < 8; i++) y[i] = E::get(h, i) * s.power * w.v[i];
         if (a.has_out) {  // one rounding to fp32 of the factor and one of the product before that to 16 bits
             const float rest = (float)s.rest;
             typename E::vec o;
@@ -134,7 +130,7 @@ __device__ __forceinline__ void put_norm(const NormArgs &a, int rank, int64_t t,
 // rows 142 us, 5.8 TB/s (a copy reaches 6.5; 150 with stores of the rows that stay in
 // the caches, 162 with a workgroup for every row and no load ahead); 8 x 8192 of 2048
 // 157, 6.0; odd ones 8 x 2048 x 1003 in fp16 25 (39 read twice). One row of 7168 takes
-// 4 us. Without a residual the arithmetic shows: 93 us, 3.8 TB/s.
+// 4 us. Without a residual the arithmetic shows: 90 us, 3.9 TB/s.
 template <typename E, int FORMAT, int VPT, int MOST, bool WHOLE>
 __global__ __launch_bounds__(MOST == kWave ? 256 : MOST) void k_norm_row(const NormArgs a) {
     __shared__ double part[2][1024 / kWave][1];

@@ -45,7 +45,7 @@ __device__ __forceinline__ double inverse_root(double m) {
 }
 
 // What a row is multiplied by, r = 1 / sqrt(mean(h^2) + eps), in two steps: a power
-// of two and the rest in double, from 1 to 2 (1/4 to 64 at the ends of bf16's range). In
+// of two and the rest in double, from 1 to 2 (to 128 for the smallest rows of bf16). In
 // types of 16 bits h * power * w is then exact in fp32 and not past its range where y is
 // not, so that an element of a block takes one product in double; but for a y below
 // 2^-132 and elements 2^-140 below their row's magnitude. (A branch for the power 1 cost
@@ -56,8 +56,8 @@ struct RowScale {
     __device__ __forceinline__ explicit RowScale(double mean) {  // of h^2, and eps
         r = inverse_root(mean);
         int k = (int)(upper_word(r) >> 20) - 1023;  // NaN, infinity and 0 at the ends
-        k = min(max(k, -126), 127);
-        power = __uint_as_float((uint32_t)(127 + k) << 23);
+        k = min(max(k, -128), 127);
+        power = __builtin_ldexpf(1.0f, k);  // may be subnormal
         rest = r * __longlong_as_double((int64_t)(1023 - k) << 52);
     }
 };

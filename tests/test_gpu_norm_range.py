@@ -49,3 +49,13 @@ def test_weights_of_all_magnitudes(H):
     near = torch.randint(-100, 112, ((H + 31) // 32,), generator=g).repeat_interleave(32)[:H]
     check([x], None, _scaled(g, 1, H, near, t)[0], M.FP8, eps=0.0)
     check([x], None, _scaled(g, 1, H, torch.randint(-80, 112, (H,), generator=g), t)[0], M.FP4, eps=0.0, want_out=False)
+
+
+@pytest.mark.parametrize("H", [64, 1003, 9000, 16392])
+def test_next_to_the_end(H):
+    """|h|, weights and y of 2^127: half of bf16's largest, a fourth of what overflows."""
+    g = torch.Generator().manual_seed(H)
+    sign = lambda n: 1 - 2 * torch.randint(0, 2, (n, H), generator=g)  # noqa: E731
+    x, w = (sign(3) * 2.0 ** 127).bfloat16(), (sign(1)[0] * 2.0 ** 127).bfloat16()
+    check([x], None, w, M.FP8, eps=0.0)
+    check([(x.double() / 2.0 ** 254).bfloat16()], None, w, M.FP4, eps=0.0)

@@ -329,7 +329,7 @@ __global__ __launch_bounds__(MOST == kWave ? 256 : MOST) void k_norm_grad_row(co
         double s[2] = {0.0, 0.0};
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
-            if (i * lanes + lane >= own) h[i] = vec{};
+            if (i * lanes + lane >= own) h[i] = g[i] = vec{};  // (an infinite g times 0 is NaN)
 #pragma unroll
             for (int c = 0; c < 8; c++) {
                 const double hc = E::get(h[i], c);

@@ -334,7 +334,8 @@ __global__ __launch_bounds__(MOST == kWave ? 256 : MOST) void k_norm_grad_row(co
             for (int c = 0; c < 8; c++) {
                 const double hc = E::get(h[i], c);
                 s[0] = __builtin_fma(hc, hc, s[0]);
-                // in 16 bits the product of two is exact in fp32
+                // In 16 bits the product is exact in fp32, inside the range that the elements' fp32
+                // below needs too (in double 8 x 2048 rows of 7168 in bf16 take 172 us, 162 so).
                 const double gw = E::kExact ? (double)(E::get(g[i], c) * E::get(w[i], c))
                                             : (double)E::get(g[i], c) * (double)E::get(w[i], c);
                 s[1] = __builtin_fma(gw, hc, s[1]);

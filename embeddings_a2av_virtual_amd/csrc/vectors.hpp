@@ -18,7 +18,9 @@ typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 // and stored is not used again soon, but for the lines of `cached` loads, which come in
 // two halves or are shared with a neighbour.
 struct ElemF32 {
-    static constexpr bool kExact = false;  // the product of two is exact in fp32
+    // The product of two is exact in fp32 where it is inside its range: of fp16 always, of
+    // bf16 from 2^-126 to 2^128.
+    static constexpr bool kExact = false;
     typedef float scalar;
     struct vec {
         f32x4 lo, hi;

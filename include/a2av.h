@@ -812,8 +812,10 @@ size_t moe_rms_norm_backward_workspace_bytes(int W, int64_t T, int64_t H);
  *   d_weight = sum over the rows of all ranks of d_out * h * r
  * d_x is the gradient of x and of the residual alike. The row's sums are in
  * double, the rest in fp32, d_x rounded once; d_weight is summed in a fixed
- * order (0 without rows). What rounds y to 8 or 4 bits has no gradient of its
- * own here: d_out is taken as y's.
+ * order (0 without rows). So r and every d_out * weight have to lie in fp32's
+ * range: rows of magnitude 2^-126 .. 2^126, products below 2^128 (past it d_x
+ * is infinite or NaN); what is below 2^-126 may be lost. What rounds y to 8 or
+ * 4 bits has no gradient of its own here: d_out is taken as y's.
  *   x[W]        device [T][H] of type: h, moe_rms_norm's sum (or its x)
  *   d_out[W]    device [T][H] of type
  *   d_sum       host array of W device [T][H] of type, or NULL

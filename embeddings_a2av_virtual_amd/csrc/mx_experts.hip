@@ -816,7 +816,7 @@ __global__ __launch_bounds__(kFewWaves *kWave, 2) void k_mx_few(const MxExpertAr
 #pragma unroll
                 for (int i = 0; i < 2 * kFewWaves; i++) t += (double)sums[i * kChunks + k][c];
                 y[c] = (float)t;
-                rest[c] = (float)(t - y[c]);  // (of an infinity NaN, as the block becomes)
+                rest[c] = __builtin_isinf(y[c]) ? 0.0f : (float)(t - y[c]);
             }
             sums[k] = y;
             sums[kChunks + k] = rest;

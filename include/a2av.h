@@ -846,11 +846,16 @@ size_t moe_expert_linear_mx_workspace_bytes(int W, int P, int64_t K, int64_t N, 
  *   h = x[d][row] . weight[d][j]^T + bias[d][j]     (fp32 sums)
  *   out[d][row] = act(h), rounded once
  * with A2AV_ACT_SWIGLU as moe_expert_linear has it (2N weight rows, N outputs).
- * Eight neighbouring products are summed exactly; but of A2AV_MX_FP8 rows with
- * an out of 16 bits a sum of eight may drop what lies more than 2^14 below its
- * largest product (5e-6 of random sums, a thousandth of out's rounding). For an
- * out of 8 bits the products of A2AV_MX_FP8 elements of 2 and above and those of
- * smaller ones have an fp32 sum each, added in double, and act is in double.
+ * Products are taken eight at a time (elements 8i .. 8i + 7) and eight are summed
+ * exactly, but of A2AV_MX_FP8 rows with an out of 16 bits where x_rows allows more
+ * than 12 rows an expert: there each is cut towards 0 at 2^-13 of the power of two
+ * below the largest of them, so that a sum of eight is off by less than 7 * 2^-13
+ * of its largest product (5e-6 of sums of random numbers; out is rounded by up to
+ * 2^-8 in bf16 and 2^-11 in fp16). Beside large products that cancel, small ones
+ * of the same eight may be gone. For an out of 8 bits, and for few rows, the
+ * products of A2AV_MX_FP8 elements of 2 and above and those of smaller ones are
+ * summed apart, which is exact; for an out of 8 bits they have an fp32 sum each,
+ * added in double, and act is in double.
  * The products read the elements as they lie: a block that stands for NaN gives
  * NaN where its row or column goes.
  *   K, N            1 .. A2AV_MAX_WIDTH

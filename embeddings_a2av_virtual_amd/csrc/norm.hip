@@ -522,10 +522,12 @@ static void launch_norm(const NormArgs &a, int W, int format, hipStream_t stream
     else launch_norm<E, 0>(a, W, stream);
 }
 
-// The gradient's: a wave each up to 2048 elements (fewer workgroups, whose weight sums
-// have to be read again: 1021 rows of 1111 in fp32 13.1 us, 18.8 with a workgroup for
-// each), else a workgroup with two vectors a thread, which leaves registers for the
-// next row, and one where there are few rows of whole vectors.
+// The gradient's: a wave each up to 1024 elements, and of many rows up to 2048 (fewer
+// workgroups, whose weight sums have to be read again; a wave or a workgroup a row: 64
+// rows of 1536 in bf16 6.7 or 5.9 us, 512 8.6 or 8.5, 2048 12 or 20, 16384 47 or 55; 64 of
+// 1111 11.9 or 9.4, 1021 15 or 19, 16384 99 or 134; in fp32 64 of 2048 7.2 or 6.1, 2048 23
+// or 31, 16384 119 or 123), else a workgroup with two vectors a thread, which leaves
+// registers for the next row's, and one where there are few rows of whole vectors.
 struct GradShape {
     bool wave;
     int per, threads;
@@ -535,7 +537,7 @@ static GradShape grad_shape(int W, int64_t T, int64_t H) {
     const int64_t vecs = (H + 7) / 8, rows = (int64_t)W * T;
     const bool whole = H % 8 == 0;
     GradShape s = {};
-    s.wave = vecs <= 256 && in_registers(H);
+    s.wave = vecs <= 128 || (vecs <= 256 && rows > 512);
     s.per = !whole ? (s.wave && vecs > 128 ? 4 : 2) : s.wave ? (int)((vecs + kWave - 1) / kWave) : vecs <= 1024 && rows < 2048 ? 1 : 2;
     if (!in_registers(H)) s.threads = 1024;
     else s.threads = s.wave ? 256 : (int)((vecs + s.per * kWave - 1) / (s.per * kWave) * kWave);

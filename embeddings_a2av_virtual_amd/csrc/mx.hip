@@ -11,7 +11,8 @@
 
 namespace a2av {
 
-// n / d for n < 2^31 by a product with a number worked out on the host.
+// n / d for n < 2^31 by a product with a number worked out on the host (division by an
+// invariant integer after Granlund and Montgomery).
 struct Divider {
     uint32_t d, magic, shift;
     explicit Divider(uint32_t by = 1) : d(by), magic(0), shift(0) {

@@ -472,7 +472,10 @@ static bool at16(const void *p) { return (uintptr_t)p % 16 == 0; }
 // Rows of the register kernels: up to 1024 threads of two vectors.
 static bool in_registers(int64_t H) { return H <= 1024 * 2 * 8; }
 static int64_t up_to(int64_t x, int64_t most) { return x < most ? x : most; }
-constexpr int kGradWaves = 4096;  // of the gradient, whose workgroups have sums of their own
+// Waves of the gradient, whose workgroups have sums of their own (2048, 4096 and 8192: 16384
+// rows of 2048 in bf16 52, 56 and 66 us, of 7168 155, 162 and 172, of 512 25, 21 and 25, of
+// 16384 495, 365 and 367).
+constexpr int kGradWaves = 4096;
 
 // A launch of a kernel that goes through `rows` rows (of each of W ranks): a few times
 // the workgroups that the compute units hold at once (8 x 2048 rows of 7168 in bf16,
@@ -487,8 +490,10 @@ static void launch_rows(K kernel, const A &a, int64_t rows, int W, int threads, 
 }
 
 // How a row is spread: a wave each up to 1024 elements, else a workgroup of just
-// enough waves; two vectors a thread leave registers for the next row's, but a few
-// rows of whole vectors are sooner done with one.
+// enough waves; two vectors a thread leave registers for the next row's, but few rows
+// of whole vectors are sooner done with one (one or two, in bf16 with residual and 8-bit
+// rows: 1 row of 4096 2.8 or 3.4 us, 1024 6.6 or 7.1, 4096 22.0 or 22.4, 16384 83.3 or
+// 82.2; of 7168 3.7 or 3.9, 13.6 or 12.5, 44 or 41, 159 or 145).
 template <typename E, int FORMAT, bool WHOLE>
 static void launch_norm(const NormArgs &a, int W, hipStream_t stream) {
     const int64_t vecs = (FORMAT ? mx_padded(a.H) : a.H + 7) / 8;
@@ -527,7 +532,9 @@ static void launch_norm(const NormArgs &a, int W, int format, hipStream_t stream
 // rows of 1536 in bf16 6.7 or 5.9 us, 512 8.6 or 8.5, 2048 12 or 20, 16384 47 or 55; 64 of
 // 1111 11.9 or 9.4, 1021 15 or 19, 16384 99 or 134; in fp32 64 of 2048 7.2 or 6.1, 2048 23
 // or 31, 16384 119 or 123), else a workgroup with two vectors a thread, which leaves
-// registers for the next row's, and one where there are few rows of whole vectors.
+// registers for the next row's, and one where there are few rows of whole vectors (one or
+// two, in bf16: 1 row of 7168 6.3 or 6.3 us, 1024 20.9 or 21.4, 4096 53 or 51, 16384 177
+// or 163; of 4096 5.6 or 5.8, 14 or 20, 31 or 37, 97 or 112).
 struct GradShape {
     bool wave;
     int per, threads;

@@ -245,8 +245,8 @@ __device__ __forceinline__ void emit(const MxExpertArgs &a, const f32x4 *sums, c
 
 // ------------------------------------------------------------------ the tiles
 // Bound by the matrix cores, their operands' LDS reads and the clock under their power:
-// 32 experts of 512 rows, K 7168, 4096 columns: 4-bit rows 271 us (3.5 PFLOP/s), 8-bit
-// ones 380 (2.5), with 8-bit outputs, two products an element, 769; K 2048, 7168
+// 32 experts of 512 rows, K 7168, 4096 columns: 4-bit rows 271 us (3.5 PFLOP/s), 291 with
+// 8-bit outputs, 8-bit ones 380 (2.5), with 8-bit outputs, two products an element, 769; K 2048, 7168
 // columns 187 and 243. Without the loads the first would take 180, with all of them
 // in the L2 240; spreading them over a step, or two steps further ahead, changes nothing.
 // Tiles of BM rows and BC columns. LDS rows are 128 bytes of an operand's row: 256
@@ -624,10 +624,11 @@ __global__ __launch_bounds__(WM *WC *kWave, 2) void k_mx_tile(const MxExpertArgs
 // workgroup has 32 output columns (gated: the gate rows and the up rows behind
 // them) of one tile of up to 16 rows; its waves take steps of 256 elements in turn,
 // and their sums meet in LDS in wave order. Every workgroup checks the offsets and
-// finds its tile in them by itself, which saves the launch of the plan. One token's 8
-// experts, K 7168 and 4096 columns: 25 us, 4.9 TB/s of weights; 32 experts of one row
-// 89, 5.6; of 8 and 16 rows 107 and 118 where tiles take 140 and 136 (K 2048, 7168
-// columns 60 and 72, tiles 62 and 62).
+// finds its tile in them by itself, which saves the launch of the plan (one row for each of
+// 32 experts, K 1024, 512 columns: 12.4 us where the rank has 32 or 512 experts, 18.3 of
+// 4096). One token's 8 experts, K 7168 and 4096 columns: 25 us, 4.9 TB/s of weights; 32
+// experts of one row 89, 5.6; of 8 and 16 rows 107 and 118 where tiles take 140 and 136
+// (K 2048, 7168 columns 60 and 72, tiles 62 and 62).
 constexpr int kFewWaves = 4, kFewCols = 32;
 constexpr int kFewMacros = 32;                       // steps of 256 elements whose scales LDS holds
 constexpr int kFewScaleRow = kFewMacros * 8 + 16;    // LDS bytes of a row of them: rows in different banks
